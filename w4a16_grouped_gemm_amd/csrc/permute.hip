@@ -6,8 +6,9 @@
 // the device (no device-to-host copy, section 2.3's concern disappears) and is
 // deterministic: atomics only count, and a slot's position is
 //   offsets[e] + #{earlier tokens routed to e},
-// computed from per-expert token bitmaps with popcounts. A token's k experts
-// are distinct, so token order alone fixes every position.
+// computed from per-expert token bitmaps with popcounts. Routing names k
+// distinct experts per token, so token order alone fixes every position; ids
+// that name an expert twice share its row.
 //
 // FlashInfer PR #7196 analysis, section 2 ("specialized BF16 permutation"):
 // copy only the valid rows, with wide vectors; rows are 16-byte aligned here
@@ -25,6 +26,18 @@ namespace {
 constexpr int kPermThreads = 1024;
 constexpr int kMaskBytes = 32 * 1024;   // LDS budget for the token bitmaps
 constexpr size_t kDynLdsMax = 144 * 1024; // dynamic LDS of one launch: bitmaps + staged ids (160 KiB per CU)
+
+// Whether slot j is the first of its token (local experts le, -1: none) that names its expert. The scatter gives
+// a token one row per expert (a bit of the expert's bitmap), so a histogram counts only such slots: a token
+// that names an expert twice then has both slots on that row, and no row is left without a slot.
+__device__ __forceinline__ bool names_first(const int (&le)[kMaxTopK], int j)
+{
+    bool first = le[j] >= 0;
+#pragma unroll
+    for (int i = 0; i < kMaxTopK; ++i)
+        first = first && (i >= j || le[i] != le[j]);
+    return first;
+}
 
 // One workgroup does the whole permutation: T*k <= 16M slots, E_loc <= 1024.
 // IDS_IN_LDS: the routing ids are read from global memory once, coalesced,
@@ -257,10 +270,15 @@ __global__ __launch_bounds__(kPermThreads) void permute_kernel(
         __syncthreads();
     } else {
     // 1. histogram of local slots
-    for (long long i = tid; i < S; i += kPermThreads) {
-        const int e = local_expert(i);
-        if (e >= 0)
-            atomicAdd(&s_count[e], 1);
+    for (int t = tid; t < T; t += kPermThreads) {
+        int le[kMaxTopK];
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+            le[j] = local_expert((long long)t * k + min(j, k - 1));
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+            if (j < k && names_first(le, j))
+                atomicAdd(&s_count[le[j]], 1);
     }
     __syncthreads();
 
@@ -381,12 +399,19 @@ __global__ __launch_bounds__(256) void permute_hist_kernel(int T, int k, int beg
     for (int e = tid; e < E; e += 256)
         s_cnt[e] = 0;
     __syncthreads();
-    const long long s0 = (long long)blockIdx.x * tpb * k;
-    const long long s1 = min((long long)T, (long long)(blockIdx.x + 1) * tpb) * k;
-    for (long long i = s0 + tid; i < s1; i += 256) {
-        const int e = ids[i] - begin;
-        if (e >= 0 && e < E)
-            atomicAdd(&s_cnt[e], 1);
+    const int t1 = (int)min((long long)T, (long long)(blockIdx.x + 1) * tpb);
+    for (int t = blockIdx.x * tpb + tid; t < t1; t += 256) {
+        int le[kMaxTopK];                     // all of the token's ids first: one round trip
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+            le[j] = ids[(long long)t * k + min(j, k - 1)] - begin;
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+            le[j] = le[j] >= 0 && le[j] < E ? le[j] : -1;
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+            if (j < k && names_first(le, j))
+                atomicAdd(&s_cnt[le[j]], 1);
     }
     __syncthreads();
     for (int e = tid; e < E; e += 256)
