@@ -225,7 +225,9 @@ size_t moe_permute_workspace_size(const moe_shape *shape);
  *   x / x_perm (both NULL, or both set): x bf16 [T][H] gathered into
  *                x_perm bf16 [T*k][H], row r = x[perm[r] / k] (rows >= R
  *                untouched)
- * Bit-exact and deterministic (no atomics decide a position).
+ * Bit-exact and deterministic (no atomics decide a position). A token that
+ * names a local expert twice has one row for it (counted once, perm holds one
+ * of the slots), and both slots' inv_perm give that row.
  * workspace: device memory of moe_permute_workspace_size(shape) bytes,
  * 4-byte aligned (NULL if that is 0); smaller -> MOE_ERR_WORKSPACE.
  */
@@ -379,6 +381,117 @@ size_t moe_w4a4_workspace_size(const moe_shape *shape);
 moe_status moe_w4a4_forward(const moe_shape *shape, const uint16_t *x, const float *router_logits,
                             const uint8_t *w13_q, const uint8_t *w13_s, const uint8_t *w2_q, const uint8_t *w2_s,
                             uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---- The W8A8 variant: int8 weights and activations, one scale per row ----
+ * Symmetric int8: a row of K codes q (two's complement, K contiguous) and one
+ * binary32 scale s stand for the values q * s. Activations have a scale per
+ * token, weights one per output channel:
+ *   w13_q int8 [E_loc][2*I][H], w13_s f32 [E_loc][2*I],
+ *   w2_q  int8 [E_loc][H][I],   w2_s  f32 [E_loc][H].
+ * The entry points that take a moe_shape require group_size == 0 (a scale's
+ * group is the whole row) and plain weights (else MOE_ERR_UNSUPPORTED). Sums
+ * of products are exact integers; scales are applied in binary32. Codes of
+ * -128 are taken as they are (the quantizers here write -127 .. 127).
+ */
+
+/*
+ * RMS norm of rows of K bf16 values (K a multiple of 8, <= 65536), with the
+ * residual's addition and an int8 output:
+ *   h = bf16(x + residual)     (h = x when residual is NULL)
+ *   v = (h * rstd) * weight,   rstd = 1 / sqrt(mean(h^2) + eps)    (binary32)
+ *   sum = h                    (given with residual, and only then)
+ *   y   = bf16(v)              (NULL: not wanted)
+ *   q   = rint(127 v / max|v|), q_scale = max|v| / 127    (NULL: not wanted)
+ * rint is to the nearest, ties to the even code, of the exact quotient up to
+ * one binary32 rounding. A row whose largest |v| is below 2^-100 gets codes
+ * and scale 0; a row with a NaN or an infinity gets codes 0 and a NaN scale,
+ * so that whatever is computed from it is NaN.
+ *   x, residual, sum, y  bf16 [rows][K]; weight bf16 [K]
+ *   q int8 [rows][K], q_scale f32 [rows]
+ * At least one of y and q. eps >= 0. sum and y may be x or residual themselves
+ * (in place); any other overlap with an output gives MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_rms_norm(int64_t rows, int32_t K, const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
+                        float eps, uint16_t *sum, uint16_t *y, int8_t *q, float *q_scale, void *stream);
+
+/*
+ * Quantize rows x K bf16 values to int8 rows, as moe_rms_norm does with its v:
+ * codes q [rows][K], scales f32 [rows]. The outputs must not overlap x.
+ */
+moe_status moe_int8_quantize(int64_t rows, int32_t K, const uint16_t *x, int8_t *q, float *q_scale, void *stream);
+
+/*
+ * Dense W8A8 product: c[m][n] = (sum_k a[m][k] * wq[n][k]) * a_scale[m] * w_scale[n].
+ *   M >= 0 (0: no-op); N a multiple of 16, <= 262144; K a multiple of 128,
+ *   <= 65536; N*K and M*K below 2^31, M*N below 2^36 (MOE_ERR_UNSUPPORTED beyond)
+ *   a int8 [M][K], a_scale f32 [M], wq int8 [N][K], w_scale f32 [N] (16-byte
+ *   aligned), c [M][N] bf16 (RNE) or f32 (c_dtype)
+ */
+moe_status moe_w8a8_dense_gemm(int32_t M, int32_t N, int32_t K, const int8_t *a, const float *a_scale, const int8_t *wq,
+                               const float *w_scale, void *c, moe_dtype c_dtype, void *stream);
+
+/*
+ * Grouped W8A8 product over expert slabs, the row semantics of
+ * moe_grouped_gemm_w4a16: for local expert e and rows r in
+ * [offsets[e], offsets[e+1]) the activation row is row a_row_index[r] / top_k
+ * of (a [T][K], a_scale [T]) when a_row_index != NULL, else row r of
+ * (a [T*k][K], a_scale [T*k]). Kinds and outputs as there (W13_SWIGLU: bf16
+ * h = silu(g) * u; W2 / W13_RAW: bf16 or f32); rows >= R of c are untouched.
+ * The grid never depends on the counts, no workspace. w_scale 16-byte aligned.
+ */
+moe_status moe_grouped_gemm_w8a8(const moe_shape *shape, moe_gemm_kind kind, const int8_t *a, const float *a_scale,
+                                 const int32_t *a_row_index, const int32_t *offsets, const int8_t *wq,
+                                 const float *w_scale, void *c, moe_dtype c_dtype, void *stream);
+
+/*
+ * The W8A8 layer after routing: permute -> gate/up (h = bf16(silu(g) * u)) ->
+ * quantize h per row -> down (y bf16) -> finalize. The rows x come quantized
+ * (moe_rms_norm or moe_int8_quantize) and the routing is the caller's (moe_route
+ * or moe_route_scored): global expert ids int32 [T][k], of which those outside
+ * [expert_begin, expert_begin + E_loc) add nothing, and weights f32 [T][k]. A
+ * token that names an expert twice gets its result twice.
+ *   x int8 [T][H], x_scale f32 [T], out bf16 [T][H] (+0.0 for a token with no
+ *   local slot); w13_s and w2_s 16-byte aligned
+ *   workspace >= moe_w8a8_workspace_size bytes (0 for an invalid shape), 256-B
+ *   aligned, no state between calls.
+ */
+size_t moe_w8a8_workspace_size(const moe_shape *shape);
+moe_status moe_w8a8_forward(const moe_shape *shape, const int8_t *x, const float *x_scale, const int32_t *topk_ids,
+                            const float *topk_w, const int8_t *w13_q, const float *w13_s, const int8_t *w2_q,
+                            const float *w2_s, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Top-k routing on scores, for routers that moe_route (softmax of the k chosen
+ * logits) does not cover. Per token, with logits l, bias b (NULL: 0):
+ *   s = sigmoid(l) or softmax(l) over all E_g, rounded to binary32
+ *   c = s + b (binary32): what the selection goes by
+ *   num_groups G > 1: group g holds experts [g E_g/G, (g+1) E_g/G); its score
+ *   is its largest c (group_top 1) or the sum of its two largest (2); only the
+ *   experts of the topk_groups best groups can be chosen
+ *   slots: the k largest c in descending order; among equals (groups too) the
+ *   lower index first
+ *   topk_w = s of the slot's expert (without b), divided by the sum of the k
+ *   chosen s if renormalize (0 where that sum is 0), times scale
+ * An expert whose logit is -inf (switched off) or whose c is NaN is chosen after
+ * all others, with weight 0.
+ *   logits f32 [T][E_g], bias f32 [E_g] -> topk_ids int32 [T][k], topk_w f32 [T][k]
+ * G divides E_g, G <= 64, 1 <= topk_groups <= G, group_top <= E_g/G,
+ * top_k <= topk_groups * E_g/G.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+    int32_t score;             /* moe_score                                      */
+    int32_t num_groups;        /* G >= 1 (1: no groups)                          */
+    int32_t topk_groups;       /* groups kept                                    */
+    int32_t group_top;         /* a group's score: its 1 or 2 best experts       */
+    int32_t renormalize;       /* weights divided by their sum                   */
+    float scale;               /* factor of the weights                          */
+} moe_router;
+
+moe_status moe_route_scored(const moe_shape *shape, const moe_router *router, const float *logits, const float *bias,
+                            int32_t *topk_ids, float *topk_w, void *stream);
 
 /*
  * Launch-shape override, for tests and tuning (not a passage of the pages: a

@@ -31,7 +31,8 @@ EXPORTED = ["moe_status_str", "moe_w4a16_check_shape", "moe_w4a16_is_supported",
             "moe_w4a16_dense_gemm", "moe_w4a16_workspace_size_shared", "moe_w4a16_forward_shared",
             "moe_w4a16_set_launch_override", "moe_w4a16_forward_noalloc", "moe_mxfp4_quantize",
             "moe_grouped_gemm_mxfp4", "moe_w4a4_workspace_size", "moe_w4a4_forward",
-            "moe_mxfp4_pack_weights"]
+            "moe_mxfp4_pack_weights", "moe_rms_norm", "moe_int8_quantize", "moe_w8a8_dense_gemm",
+            "moe_grouped_gemm_w8a8", "moe_w8a8_workspace_size", "moe_w8a8_forward", "moe_route_scored"]
 
 
 class MoeShape(ctypes.Structure):
@@ -39,6 +40,11 @@ class MoeShape(ctypes.Structure):
                 ("num_experts", ctypes.c_int32), ("expert_begin", ctypes.c_int32),
                 ("num_local_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("group_size", ctypes.c_int32), ("weight_layout", ctypes.c_int32)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class LaunchOverride(ctypes.Structure):
@@ -113,6 +119,21 @@ def load_library(path: str = LIB_PATH):
         lib.moe_w4a4_forward.restype = I
         lib.moe_mxfp4_pack_weights.argtypes = [S, I, P, P, P]
         lib.moe_mxfp4_pack_weights.restype = I
+        i32, F = ctypes.c_int32, ctypes.c_float
+        lib.moe_rms_norm.argtypes = [ctypes.c_int64, i32, P, P, P, F, P, P, P, P, P]
+        lib.moe_rms_norm.restype = I
+        lib.moe_int8_quantize.argtypes = [ctypes.c_int64, i32, P, P, P, P]
+        lib.moe_int8_quantize.restype = I
+        lib.moe_w8a8_dense_gemm.argtypes = [i32, i32, i32, P, P, P, P, P, I, P]
+        lib.moe_w8a8_dense_gemm.restype = I
+        lib.moe_grouped_gemm_w8a8.argtypes = [S, I, P, P, P, P, P, P, P, I, P]
+        lib.moe_grouped_gemm_w8a8.restype = I
+        lib.moe_w8a8_workspace_size.argtypes = [S]
+        lib.moe_w8a8_workspace_size.restype = Z
+        lib.moe_w8a8_forward.argtypes = [S, P, P, P, P, P, P, P, P, P, P, Z, P]
+        lib.moe_w8a8_forward.restype = I
+        lib.moe_route_scored.argtypes = [S, ctypes.POINTER(Router), P, P, P, P, P]
+        lib.moe_route_scored.restype = I
         _lib = lib
         return lib
 
@@ -543,4 +564,221 @@ def moe_w4a4_forward(x: torch.Tensor, router_logits: torch.Tensor, w13_q: torch.
     _check(lib.moe_w4a4_forward(ctypes.byref(sh), _ptr(x), _ptr(router_logits), _ptr(w13_q), _ptr(w13_s),
                                 _ptr(w2_q), _ptr(w2_s), _ptr(out), _ptr(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the W8A8 variant: int8 rows with one float32 scale each; the RMS norm that
+# makes such rows; routing on scores
+# ---------------------------------------------------------------------------
+
+class _launch_on:
+    """Where a call runs: on `stream`, else on the current stream of the tensors' device. Inside, that device and
+    stream are current, so what the call allocates belongs to the stream that writes it."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if stream is None:
+            if device.index != torch.cuda.current_device():
+                self.guards.append(torch.cuda.device(device))
+        elif isinstance(stream, torch.cuda.Stream):
+            self.guards.append(torch.cuda.stream(stream))
+        else:
+            self.guards.append(torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device)))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in self.guards:
+            g.__exit__(*exc)
+        return False
+
+
+def _need_all(device, *tensors):
+    """(tensor, dtype, shape, name): dtype, contiguity, device and shape; None entries are skipped."""
+    for t, dtype, shape, name in tensors:
+        if t is None:
+            continue
+        _need(t, dtype, name)
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _out_dtype(out, out_dtype):
+    dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(out_dtype if out is None else out.dtype)
+    if dt is None:
+        raise ValueError("out dtype must be bfloat16 or float32")
+    return dt
+
+
+def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None = None, score: str = "sigmoid",
+                 num_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalize: bool = True,
+                 scale: float = 1.0, stream=None):
+    """Top-k routing on scores -> (topk_ids int32 [T,k], topk_w float32 [T,k]); see moe_route_scored in the C header.
+
+    score: "sigmoid" or "softmax" (over all experts). bias [E] is added for the selection only. With num_groups > 1
+    only the experts of the topk_groups best groups are chosen from (a group's score: its best expert, or the sum of
+    its two best with group_top=2). Weights are the scores, divided by their sum (renormalize), times scale."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    _need_all(logits.device, (logits, torch.float32, (T, E), "logits"), (bias, torch.float32, (E,), "bias"))
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    r = Router(int(score == "sigmoid"), int(num_groups), int(topk_groups), int(group_top), int(bool(renormalize)),
+               float(scale))
+    sh = make_shape(T, 128, 128, E, E, top_k)
+    with _launch_on(logits.device, stream) as st:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        _check(load_library().moe_route_scored(ctypes.byref(sh), ctypes.byref(r), _ptr(logits), _ptr(bias), _ptr(ids),
+                                               _ptr(w), st))
+    return ids, w
+
+
+def _rms_norm(x, residual, weight, eps, sum_out, bf16, int8, stream):
+    _need(x, torch.bfloat16, "x")
+    K, dev = x.shape[-1], x.device
+    rows = x.numel() // K if K else 0
+    _need_all(dev, (residual, torch.bfloat16, x.shape, "residual"), (weight, torch.bfloat16, (K,), "weight"),
+              (sum_out, torch.bfloat16, x.shape, "sum_out"))
+    with _launch_on(dev, stream) as st:
+        if residual is not None and sum_out is None:
+            sum_out = torch.empty_like(x)
+        y = torch.empty_like(x) if bf16 else None
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev) if int8 else None
+        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if int8 else None
+        _check(load_library().moe_rms_norm(rows, K, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(sum_out),
+                                           _ptr(y), _ptr(q), _ptr(s), st))
+    return y, q, s, sum_out
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, stream=None) -> torch.Tensor:
+    """RMS norm of the rows of x (bf16, last dimension), times weight."""
+    return _rms_norm(x, None, weight, eps, None, True, False, stream)[0]
+
+
+def add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                 sum_out: torch.Tensor | None = None, stream=None):
+    """(RMS norm of x + residual, x + residual), both bf16. sum_out may be residual or x itself (in place)."""
+    if residual is None:
+        raise ValueError("residual is required")
+    y, _, _, h = _rms_norm(x, residual, weight, eps, sum_out, True, False, stream)
+    return y, h
+
+
+def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, with_bf16: bool = False, stream=None):
+    """RMS norm with int8 rows: (codes int8, scales float32 per row[, the bf16 rows])."""
+    y, q, s, _ = _rms_norm(x, None, weight, eps, None, with_bf16, True, stream)
+    return (q, s, y) if with_bf16 else (q, s)
+
+
+def add_rms_norm_int8(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                      sum_out: torch.Tensor | None = None, with_bf16: bool = False, stream=None):
+    """RMS norm of x + residual with int8 rows: (codes int8, scales float32 per row, x + residual[, the bf16 rows]).
+
+    sum_out may be residual or x itself (in place). with_bf16: a router reads the unquantized rows."""
+    if residual is None:
+        raise ValueError("residual is required")
+    y, q, s, h = _rms_norm(x, residual, weight, eps, sum_out, with_bf16, True, stream)
+    return (q, s, h, y) if with_bf16 else (q, s, h)
+
+
+def int8_quantize(x: torch.Tensor, *, stream=None):
+    """bf16 rows -> (codes int8, scales float32 per row): code * scale stands for the value."""
+    _need(x, torch.bfloat16, "x")
+    K = x.shape[-1]
+    with _launch_on(x.device, stream) as st:
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _check(load_library().moe_int8_quantize(x.numel() // K if K else 0, K, _ptr(x), _ptr(q), _ptr(s), st))
+    return q, s
+
+
+def dense_gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, *,
+                    out_dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Dense W8A8 product: c [M, N] = (a [M, K] . wq [N, K]^T) * a_scale [M] * w_scale [N]."""
+    if a.dim() != 2 or wq.dim() != 2:
+        raise ValueError("a must be [M, K] and wq [N, K]")
+    M, K = a.shape
+    N, dev = wq.shape[0], a.device
+    dt = _out_dtype(out, out_dtype)
+    _need_all(dev, (a, torch.int8, (M, K), "a"), (a_scale, torch.float32, (M,), "a_scale"),
+              (wq, torch.int8, (N, K), "wq"), (w_scale, torch.float32, (N,), "w_scale"),
+              (out, None if out is None else out.dtype, (M, N), "out"))
+    with _launch_on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        _check(load_library().moe_w8a8_dense_gemm(M, N, K, _ptr(a), _ptr(a_scale), _ptr(wq), _ptr(w_scale), _ptr(out),
+                                                  dt, st))
+    return out
+
+
+def grouped_gemm_w8a8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor, wq: torch.Tensor,
+                      w_scale: torch.Tensor, *, num_tokens: int, top_k: int, a_row_index: torch.Tensor | None = None,
+                      out_dtype=torch.bfloat16, num_experts: int | None = None, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Grouped W8A8 product over expert slabs; returns c [num_tokens*top_k, cols] (rows past the last routed one
+    are not written). kind, offsets and a_row_index as in grouped_gemm_w4a16."""
+    if wq.dim() != 3:
+        raise ValueError("wq must be [E, N, K]")
+    E_loc, N, K = wq.shape
+    dev = a.device
+    H, I = (N, K) if kind == W2 else (K, N // 2)
+    cols = I if kind == W13_SWIGLU else N
+    rows = num_tokens * top_k
+    a_rows = rows if a_row_index is None else num_tokens
+    dt = _out_dtype(out, out_dtype)
+    _need_all(dev, (a, torch.int8, (a_rows, K), "a"), (a_scale, torch.float32, (a_rows,), "a_scale"),
+              (offsets, torch.int32, (E_loc + 1,), "offsets"), (wq, torch.int8, (E_loc, N, K), "wq"),
+              (w_scale, torch.float32, (E_loc, N), "w_scale"), (a_row_index, torch.int32, (rows,), "a_row_index"),
+              (out, None if out is None else out.dtype, (rows, cols), "out"))
+    sh = make_shape(num_tokens, H, I, num_experts or E_loc, E_loc, top_k, group_size=0)
+    with _launch_on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        _check(load_library().moe_grouped_gemm_w8a8(ctypes.byref(sh), int(kind), _ptr(a), _ptr(a_scale),
+                                                    _ptr(a_row_index), _ptr(offsets), _ptr(wq), _ptr(w_scale),
+                                                    _ptr(out), dt, st))
+    return out
+
+
+def moe_w8a8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                     w13_q: torch.Tensor, w13_s: torch.Tensor, w2_q: torch.Tensor, w2_s: torch.Tensor,
+                     out: torch.Tensor | None = None, stream=None, *, num_experts: int | None = None,
+                     expert_begin: int = 0, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The W8A8 expert layer after routing: x int8 [T, H] with x_scale [T] (add_rms_norm_int8, int8_quantize),
+    topk_ids / topk_w from route or route_scored, weights int8 [E_loc, 2I, H] / [E_loc, H, I] with a float32 scale per
+    row. num_experts: the router's (default: all local). Returns out bf16 [T, H]."""
+    if x.dim() != 2 or topk_ids.dim() != 2 or w13_q.dim() != 3:
+        raise ValueError("x must be [T, H], topk_ids [T, k] and w13_q [E, 2I, H]")
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E_loc, N13, _ = w13_q.shape
+    I, dev = N13 // 2, x.device
+    _need_all(dev, (x, torch.int8, (T, H), "x"), (x_scale, torch.float32, (T,), "x_scale"),
+              (topk_ids, torch.int32, (T, k), "topk_ids"), (topk_w, torch.float32, (T, k), "topk_w"),
+              (w13_q, torch.int8, (E_loc, 2 * I, H), "w13_q"), (w13_s, torch.float32, (E_loc, 2 * I), "w13_s"),
+              (w2_q, torch.int8, (E_loc, H, I), "w2_q"), (w2_s, torch.float32, (E_loc, H), "w2_s"),
+              (out, torch.bfloat16, (T, H), "out"))
+    sh = make_shape(T, H, I, num_experts or expert_begin + E_loc, E_loc, k, expert_begin, group_size=0)
+    lib = load_library()
+    with _launch_on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        nbytes = int(lib.moe_w8a8_workspace_size(ctypes.byref(sh)))
+        if workspace is None:
+            # from the caching allocator at every call (about 1 us): it belongs to this stream, or to the graph that
+            # is being captured, so no two calls that can overlap share one
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        _check(lib.moe_w8a8_forward(ctypes.byref(sh), _ptr(x), _ptr(x_scale), _ptr(topk_ids), _ptr(topk_w), _ptr(w13_q),
+                                    _ptr(w13_s), _ptr(w2_q), _ptr(w2_s), _ptr(out), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), st))
     return out
