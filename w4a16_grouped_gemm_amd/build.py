@@ -3,7 +3,8 @@
 Flags: gfx950 only; -O3; no FP contraction (the combine must be exactly the
 IEEE multiply / FMA it names); fp32 denormals preserved (no flush-to-zero);
 packed-fp32 instructions disabled; MFMA accumulators in ordinary VGPRs
-(the epilogue reads them with plain VALU instructions, no AGPR copies).
+(the epilogue reads them with plain VALU instructions, no AGPR copies), but
+for the W8A8 products, whose largest tile holds 256 of them per lane.
 """
 from __future__ import annotations
 
@@ -24,13 +25,16 @@ SOURCES = ["api.hip", "route.hip", "permute.hip", "gemm_w4a16.hip", "decode.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-fno-gpu-flush-denormals-to-zero", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-         "-mllvm", "-amdgpu-mfma-vgpr-form=1",
          "-Wall", "-Wno-unused-function", "-I" + INCLUDE, "-I" + CSRC]
+# Accumulators in ordinary VGPRs, except where a wave holds more of them than there are (256)
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+AGPR_SOURCES = {"gemm_w8a8.hip"}
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    flags = FLAGS if src in AGPR_SOURCES else FLAGS + VGPR_FORM
+    cmd = [HIPCC, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")

@@ -7,6 +7,8 @@
 // MFMA: v_mfma_i32_16x16x64_i8, the weight rows as operand A and the tokens as
 // operand B, so that a result lane holds four consecutive outputs of one token.
 // Both operands take the same permutation of K, which leaves the sums as they are.
+#include <mutex>
+
 #include "gemm_core.hpp"
 #include "w8a8.hpp"
 
@@ -186,11 +188,259 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Many rows per expert: a workgroup of four waves computes BN weight rows x BM
+// tokens, a wave 32 TN x 32 TM of them with v_mfma_i32_32x32x32_i8. Both
+// operands pass through LDS, kStageK bytes of K to a stage, four stages deep.
+//
+// A stage holds BN + BM rows of 64 bytes, four 16-byte chunks each; row r keeps
+// chunk c at place c ^ ((r >> 2) & 3), so that the 64 lanes of a fragment read
+// (32 rows x 2 chunks) meet no bank conflict. The copies go from memory straight
+// to LDS (buffer_load ... lds, 16 bytes a lane, lane l to place l of 16 rows);
+// each lane asks for the chunk that belongs to its place, so four lanes still
+// read 64 contiguous bytes.
+//
+// A weight row's place decides which output a result register is: tile t's row
+// r holds output ((r >> 2) & 1) 16 TG + 16 t + 4 (r >> 3) + (r & 3) of the
+// wave's columns, which makes a lane's sixteen results of a tile consecutive.
+// ---------------------------------------------------------------------------
+constexpr int kStageK = 64;
+constexpr int kStages = 4;
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+
+constexpr uint32_t vmcnt_imm(int n)                   // s_waitcnt vmcnt(n) lgkmcnt(0)
+{
+    return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4));
+}
+
+// 16 bytes per lane from memory to LDS: lane l's to dst + 16 l
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, lds_byte *dst, uint32_t voff, uint32_t soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(N));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tile (row tile, column tile) of linear index i: column tiles in groups of
+// eight row tiles, so that the workgroups running at one time share both operands.
+__device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
+{
+    constexpr int G = 8;
+    const int g = i / (G * tn), rest = i - g * G * tn;
+    const int gm = tm - g * G < G ? tm - g * G : G;
+    m = g * G + rest % gm;
+    n = rest / gm;
+}
+
+template <int TN, int TM>
+struct Frags {
+    u32x4 w[TN], x[TM];
+};
+
+template <int KIND, bool F32, int TN, int TM, int NWN, int NWM>
+__global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int tn)
+{
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    constexpr int TG = SW ? TN / 2 : TN;
+    constexpr int BN = 32 * TN * NWN, BM = 32 * TM * NWM;
+    constexpr int BC = SW ? BN / 2 : BN;                // output columns of the workgroup
+    constexpr int LN = BN / 64, LM = BM / 64;           // copies of a wave per stage
+    constexpr int L = LN + LM;
+    constexpr int kStageBytes = (BN + BM) * kStageK;
+    extern __shared__ __align__(16) unsigned char s_dyn[];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int wn = wave / NWM, wm = wave % NWM;
+    // XCD x (workgroups x, x + 8, ...) takes the x-th share of the tiles
+    const int total = gridDim.x, per = total / kXcds, extra = total % kXcds;
+    const int x = blockIdx.x % kXcds;
+    const int item = x * per + (x < extra ? x : extra) + blockIdx.x / kXcds;
+    int mt, nt;
+    tile_of(item, tm, tn, mt, nt);
+    int e, r0, rows;
+    if (!find_chunk(p, BM, mt, lane, e, r0, rows))
+        return;
+    e = uniform(e);
+    const int cols = SW ? p.N / 2 : p.N;
+    const int n0 = nt * BC;
+    const uint32_t K = (uint32_t)p.K;
+
+    // this lane's place in a copy of 16 rows, and the chunk that belongs there
+    const int prow = lane >> 2;
+    auto chunk_at = [&](int row) { return (uint32_t)(((lane & 3) ^ ((row >> 2) & 3)) * 16); };
+    uint32_t wo[LN], xo[LM];
+#pragma unroll
+    for (int j = 0; j < LN; ++j) {
+        const int row = (wave * LN + j) * 16 + prow;    // row of the stage: wave's columns, tile, row of the tile
+        const int w = row / (32 * TN), t = row / 32 % TN, r = row % 32;
+        int n = n0 + w * 32 * TG + ((r >> 2) & 1) * 16 * TG + (t % TG) * 16 + (r >> 3) * 4 + (r & 3);
+        n = n < cols ? n : cols - 1;
+        wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + chunk_at(row);
+    }
+#pragma unroll
+    for (int j = 0; j < LM; ++j) {
+        const int row = (wave * LM + j) * 16 + prow;
+        xo[j] = (uint32_t)act_row(p, r0 + (row < rows ? row : rows - 1)) * K + chunk_at(row);
+    }
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * K, (uint32_t)p.N * K);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, 0xFFFFFFFFu);
+    lds_byte *lds = (lds_byte *)s_dyn;
+    auto copy = [&](int s) {                            // stage of K bytes [64 s, 64 s + 64)
+        lds_byte *dst = lds + (s & (kStages - 1)) * kStageBytes;
+        const uint32_t k = (uint32_t)s * kStageK;
+#pragma unroll
+        for (int j = 0; j < LN; ++j)
+            copy16(rw, dst + (wave * LN + j) * 1024, wo[j], k);
+#pragma unroll
+        for (int j = 0; j < LM; ++j)
+            copy16(rx, dst + BN * kStageK + (wave * LM + j) * 1024, xo[j], k);
+    };
+    // fragment reads: lane l holds chunk 2 kk + l / 32 of row l % 32
+    const int fr = lane & 31;
+    const uint32_t f0 = (uint32_t)(fr * 64 + (((lane >> 5) ^ ((fr >> 2) & 3)) * 16));
+    const uint32_t f1 = f0 ^ 32u;
+    using Fr = Frags<TN, TM>;
+    auto read = [&](int s, uint32_t f, Fr &d) {
+        const unsigned char *src = s_dyn + (s & (kStages - 1)) * kStageBytes + f;
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+            d.w[t] = *reinterpret_cast<const u32x4 *>(src + (wn * TN + t) * 2048);
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+            d.x[t] = *reinterpret_cast<const u32x4 *>(src + BN * kStageK + (wm * TM + t) * 2048);
+    };
+    i32x16 acc[TN][TM];
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+        for (int b = 0; b < TM; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[a][b][i] = 0;
+    auto multiply = [&](const Fr &d) {
+#pragma unroll
+        for (int a = 0; a < TN; ++a)
+#pragma unroll
+            for (int b = 0; b < TM; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, d.w[a]),
+                                                                  __builtin_bit_cast(i32x4, d.x[b]), acc[a][b], 0, 0, 0);
+    };
+    // Step s multiplies stage s. In its middle the wave waits for its copies of
+    // stage s + 1 (those of s + 2 and s + 3 stay in flight) and meets the other
+    // waves: then stage s + 1 is whole, and stage s, all of whose reads are
+    // done, takes the copies of stage s + 4. The second half's fragments are in
+    // registers by then, so the matrix unit has work while the first half's of
+    // the next step are read.
+    const int steps = p.K / kStageK;                    // even
+    Fr d0, d1;
+    copy(0);
+    copy(1);
+    if (steps > 2) {
+        copy(2);
+        copy(3);
+        wait_barrier<3 * L>();
+    } else {
+        wait_barrier<L>();
+    }
+    read(0, f0, d0);
+    int s = 0;
+    for (; s + 4 < steps; ++s) {
+        read(s, f1, d1);
+        multiply(d0);
+        wait_barrier<2 * L>();
+        copy(s + 4);
+        read(s + 1, f0, d0);
+        multiply(d1);
+    }
+    for (; s < steps; ++s) {                            // the last four steps: nothing left to copy
+        read(s, f1, d1);
+        multiply(d0);
+        wait_barrier<0>();
+        if (s + 1 < steps)
+            read(s + 1, f0, d0);
+        multiply(d1);
+    }
+
+    const int half = lane >> 5, m32 = lane & 31;
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int m = (wm * TM + b) * 32 + m32;
+        if (m >= rows)
+            continue;
+        const float as = p.as[act_row(p, r0 + m)];
+        const size_t crow = (size_t)(r0 + m) * cols;
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int n = n0 + wn * 32 * TG + half * 16 * TG + t * 16 + g * 4;
+                if (n >= cols)
+                    continue;
+                const float *ws = p.ws + (size_t)e * p.N + n;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = (float)acc[t][b][4 * g + i] * as * ws[i];
+                    if constexpr (SW)
+                        v[i] = silu_fast(v[i]) * ((float)acc[t + TG][b][4 * g + i] * as * ws[cols + i]);
+                }
+                if constexpr (F32)
+                    *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + crow + n) = floatx4{v[0], v[1], v[2], v[3]};
+                else
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + crow + n) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            }
+        }
+    }
+}
+
+template <int KIND, bool F32, int TN, int TM, int NWN, int NWM>
+void allow_lds(int bytes)
+{
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int KIND, bool F32, int TN, int TM, int NWN, int NWM>
+hipError_t launch_tile(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
+{
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    constexpr int BN = 32 * TN * NWN, BM = 32 * TM * NWM, BC = SW ? BN / 2 : BN;
+    constexpr int lds = (BN + BM) * kStageK * kStages;
+    const int cols = SW ? g.N / 2 : g.N;
+    const int tn = (cols + BC - 1) / BC;
+    const int tm = g.offsets ? g.max_rows / BM + (g.num_experts < g.max_rows ? g.num_experts : g.max_rows)
+                             : (g.max_rows + BM - 1) / BM;
+    static std::once_flag once;
+    std::call_once(once, allow_lds<KIND, F32, TN, TM, NWN, NWM>, lds);
+    hipLaunchKernelGGL((w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM>), dim3((unsigned)(tm * tn)), dim3(256), lds, st, p,
+                       tm, tn);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_w8_gemm(const W8GemmLaunch &g, hipStream_t st)
 {
     const W8Args p{g.a, g.as, g.a_row_index, g.top_k, g.offsets, g.max_rows, g.num_experts, g.wq, g.ws, g.c, g.K, g.N};
+    const int per_expert = g.expected_rows / (g.num_experts > 0 ? g.num_experts : 1);
+    if (per_expert > 64) {
+        if (g.kind == MOE_GEMM_W13_SWIGLU)
+            return launch_tile<MOE_GEMM_W13_SWIGLU, false, 4, 4, 2, 2>(g, p, st);
+        if (g.c_f32)
+            return launch_tile<MOE_GEMM_W2, true, 4, 4, 2, 2>(g, p, st);
+        return launch_tile<MOE_GEMM_W2, false, 4, 4, 2, 2>(g, p, st);
+    }
     if (g.kind == MOE_GEMM_W13_SWIGLU)
         return launch_stream<MOE_GEMM_W13_SWIGLU, false>(g, p, st);
     if (g.c_f32)
