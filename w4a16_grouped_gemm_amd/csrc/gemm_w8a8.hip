@@ -23,6 +23,14 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 w, u32x4 x, i32x4 c)
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), c, 0, 0, 0);
 }
 
+// fp32 pair -> bf16 pair, round to nearest even
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
+}
+
 struct W8Args {
     const int8_t *a;
     const float *as;
@@ -243,6 +251,26 @@ __device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
     n = rest / gm;
 }
 
+// The order of a half step's instructions: LDS reads first, then copies to LDS,
+// as few as possible behind each MFMA, so that none of them holds the matrix
+// unit's next instruction back and the reads are done before the half step ends.
+template <int MFMAS, int READS, int COPIES>
+__device__ __forceinline__ void spread()
+{
+    constexpr int kPer = (READS + COPIES + MFMAS - 1) / MFMAS;
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+        for (int j = i * kPer; j < (i + 1) * kPer; ++j) {
+            if (j < READS)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            else if (j < READS + COPIES)
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+    }
+}
+
 template <int TN, int TM>
 struct Frags {
     u32x4 w[TN], x[TM];
@@ -357,10 +385,12 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
     for (; s + 4 < steps; ++s) {
         read(s, f1, d1);
         multiply(d0);
+        spread<TN * TM, TN + TM, 0>();
         wait_barrier<2 * L>();
-        copy(s + 4);
         read(s + 1, f0, d0);
+        copy(s + 4);
         multiply(d1);
+        spread<TN * TM, TN + TM, L>();
     }
     for (; s < steps; ++s) {                            // the last four steps: nothing left to copy
         read(s, f1, d1);
@@ -371,36 +401,71 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
         multiply(d1);
     }
 
+    // Epilogue: 32 tokens at a time through the wave's own part of LDS (all
+    // reads of the stages are done), so that a store writes whole runs of a row
+    // (16 TG or 32 TG lanes' worth) instead of 8 bytes per token.
+    __syncthreads();
+    constexpr int kElem = F32 ? 4 : 2;
+    constexpr int kRow = 32 * TG * kElem;               // bytes of a row in the wave's columns
+    constexpr int kPitch = kRow + 16;
+    constexpr int kLanes = kRow / 16;                   // lanes that store a row
+    static_assert(32 * kPitch * 4 <= kStageBytes * kStages, "the epilogue's rows fit the stages");
+    unsigned char *buf = s_dyn + wave * (32 * kPitch);
     const int half = lane >> 5, m32 = lane & 31;
+    const int nw = n0 + wn * 32 * TG;                   // the wave's first column
+    const float *wsp = p.ws + (size_t)e * p.N;
+    float wsv[TN][16];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            int n = nw + half * 16 * TG + (t % TG) * 16 + g * 4;
+            n = (n < cols ? n : cols - 4) + (SW && t >= TG ? cols : 0);
+            const floatx4 v = *reinterpret_cast<const floatx4 *>(wsp + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                wsv[t][4 * g + i] = v[i];
+        }
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
-        const int m = (wm * TM + b) * 32 + m32;
-        if (m >= rows)
-            continue;
-        const float as = p.as[act_row(p, r0 + m)];
-        const size_t crow = (size_t)(r0 + m) * cols;
+        const int mb = (wm * TM + b) * 32;
+        if (mb >= rows)
+            break;
+        const int m = mb + m32;
+        const float as = p.as[act_row(p, r0 + (m < rows ? m : rows - 1))];
 #pragma unroll
         for (int t = 0; t < TG; ++t) {
+            float v[16];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int n = n0 + wn * 32 * TG + half * 16 * TG + t * 16 + g * 4;
-                if (n >= cols)
-                    continue;
-                const float *ws = p.ws + (size_t)e * p.N + n;
-                float v[4];
+            for (int i = 0; i < 16; ++i) {
+                v[i] = (float)acc[t][b][i] * as * wsv[t][i];
+                if constexpr (SW)
+                    v[i] = silu_fast(v[i]) * ((float)acc[t + TG][b][i] * as * wsv[t + TG][i]);
+            }
+            u32x4 *dst = reinterpret_cast<u32x4 *>(buf + m32 * kPitch + (half * 16 * TG + t * 16) * kElem);
+            if constexpr (F32) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = (float)acc[t][b][4 * g + i] * as * ws[i];
-                    if constexpr (SW)
-                        v[i] = silu_fast(v[i]) * ((float)acc[t + TG][b][4 * g + i] * as * ws[cols + i]);
-                }
-                if constexpr (F32)
-                    *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + crow + n) = floatx4{v[0], v[1], v[2], v[3]};
-                else
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + crow + n) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                for (int g = 0; g < 4; ++g)
+                    dst[g] = __builtin_bit_cast(u32x4, floatx4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]});
+            } else {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    dst[g] = u32x4{bf16_pair(v[8 * g], v[8 * g + 1]), bf16_pair(v[8 * g + 2], v[8 * g + 3]),
+                                   bf16_pair(v[8 * g + 4], v[8 * g + 5]), bf16_pair(v[8 * g + 6], v[8 * g + 7])};
             }
         }
+        // the wave's own writes, in order before its reads
+        __builtin_amdgcn_wave_barrier();
+        const int at = lane % kLanes, n = nw + at * (16 / kElem);
+#pragma unroll
+        for (int j = 0; j < 32 * kLanes / 64; ++j) {
+            const int row = j * (64 / kLanes) + lane / kLanes;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(buf + row * kPitch + at * 16);
+            if (mb + row < rows && n < cols)
+                *reinterpret_cast<u32x4 *>(static_cast<unsigned char *>(p.c) +
+                                           ((size_t)(r0 + mb + row) * cols + n) * kElem) = v;
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
