@@ -199,7 +199,7 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // ---------------------------------------------------------------------------
 // Many rows per expert: a workgroup of four waves computes BN weight rows x BM
 // tokens, a wave 32 TN x 32 TM of them with v_mfma_i32_32x32x32_i8. Both
-// operands pass through LDS, kStageK bytes of K to a stage, four stages deep.
+// operands pass through LDS, kStageK bytes of K to a stage, five stages deep.
 //
 // A stage holds BN + BM rows of 64 bytes, four 16-byte chunks each; row r keeps
 // chunk c at place c ^ ((r >> 2) & 3), so that the 64 lanes of a fragment read
@@ -213,14 +213,14 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // wave's columns, which makes a lane's sixteen results of a tile consecutive.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 64;
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) unsigned char lds_byte;
 
-constexpr uint32_t vmcnt_imm(int n)                   // s_waitcnt vmcnt(n) lgkmcnt(0)
+constexpr uint32_t vmcnt_imm(int n)                   // s_waitcnt vmcnt(n), other counters untouched
 {
-    return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4));
+    return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
 // 16 bytes per lane from memory to LDS: lane l's to dst + 16 l
@@ -251,23 +251,24 @@ __device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
     n = rest / gm;
 }
 
-// The order of a half step's instructions: LDS reads first, then copies to LDS,
-// as few as possible behind each MFMA, so that none of them holds the matrix
-// unit's next instruction back and the reads are done before the half step ends.
+// How many of n things spread evenly over m places come before place i.
+constexpr int spread_to(int i, int n, int m) { return i * n / m; }
+
+// The order of a half step's instructions: its LDS reads and its copies to LDS
+// spread evenly behind the MFMAs, so that none of them holds the matrix unit's
+// next instruction back. (The half step issues them in this order already.)
 template <int MFMAS, int READS, int COPIES>
 __device__ __forceinline__ void spread()
 {
-    constexpr int kPer = (READS + COPIES + MFMAS - 1) / MFMAS;
 #pragma unroll
     for (int i = 0; i < MFMAS; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
 #pragma unroll
-        for (int j = i * kPer; j < (i + 1) * kPer; ++j) {
-            if (j < READS)
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            else if (j < READS + COPIES)
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        }
+        for (int j = spread_to(i, READS, MFMAS); j < spread_to(i + 1, READS, MFMAS); ++j)
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+        for (int j = spread_to(i, COPIES, MFMAS); j < spread_to(i + 1, COPIES, MFMAS); ++j)
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
 }
 
@@ -323,29 +324,30 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * K, (uint32_t)p.N * K);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, 0xFFFFFFFFu);
     lds_byte *lds = (lds_byte *)s_dyn;
-    auto copy = [&](int s) {                            // stage of K bytes [64 s, 64 s + 64)
-        lds_byte *dst = lds + (s & (kStages - 1)) * kStageBytes;
-        const uint32_t k = (uint32_t)s * kStageK;
+    // one of a wave's L copies of a stage: K bytes [k, k + 64) to the stage at byte `at` of LDS
+    auto copy_one = [&](int j, uint32_t at, uint32_t k) {
+        lds_byte *dst = lds + at;
+        if (j < LN)
+            copy16(rw, dst + (wave * LN + j) * 1024, wo[j < LN ? j : 0], k);
+        else
+            copy16(rx, dst + BN * kStageK + (wave * LM + j - LN) * 1024, xo[j < LN ? 0 : j - LN], k);
+    };
+    auto copy = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < LN; ++j)
-            copy16(rw, dst + (wave * LN + j) * 1024, wo[j], k);
-#pragma unroll
-        for (int j = 0; j < LM; ++j)
-            copy16(rx, dst + BN * kStageK + (wave * LM + j) * 1024, xo[j], k);
+        for (int j = 0; j < L; ++j)
+            copy_one(j, (uint32_t)(s % kStages) * kStageBytes, (uint32_t)s * kStageK);
     };
     // fragment reads: lane l holds chunk 2 kk + l / 32 of row l % 32
     const int fr = lane & 31;
     const uint32_t f0 = (uint32_t)(fr * 64 + (((lane >> 5) ^ ((fr >> 2) & 3)) * 16));
     const uint32_t f1 = f0 ^ 32u;
     using Fr = Frags<TN, TM>;
-    auto read = [&](int s, uint32_t f, Fr &d) {
-        const unsigned char *src = s_dyn + (s & (kStages - 1)) * kStageBytes + f;
-#pragma unroll
-        for (int t = 0; t < TN; ++t)
-            d.w[t] = *reinterpret_cast<const u32x4 *>(src + (wn * TN + t) * 2048);
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-            d.x[t] = *reinterpret_cast<const u32x4 *>(src + BN * kStageK + (wm * TM + t) * 2048);
+    // one of a half step's TN + TM fragments (tokens and the first weights first: what the MFMAs need first)
+    auto read_one = [&](int j, const unsigned char *src, Fr &d) {
+        if (j < TM)
+            d.x[j < TM ? j : 0] = *reinterpret_cast<const u32x4 *>(src + BN * kStageK + (wm * TM + j) * 2048);
+        else
+            d.w[j < TM ? 0 : j - TM] = *reinterpret_cast<const u32x4 *>(src + (wn * TN + j - TM) * 2048);
     };
     i32x16 acc[TN][TM];
 #pragma unroll
@@ -355,54 +357,89 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 acc[a][b][i] = 0;
-    auto multiply = [&](const Fr &d) {
+    // Half a step: multiplies d while the fragments at byte `from` of LDS go to
+    // dn and copies [C0, C1) of the stage at byte `to` go out.
+    auto half_step = [&](const Fr &d, Fr &dn, uint32_t from, auto c0, auto c1, uint32_t to, uint32_t k) {
+        constexpr int M = TN * TM, R = TN + TM, C0 = decltype(c0)::value, C = decltype(c1)::value - C0;
+        const unsigned char *src = s_dyn + from;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+#pragma unroll
+            for (int j = spread_to(i, R, M); j < spread_to(i + 1, R, M); ++j)
+                read_one(j, src, dn);
+#pragma unroll
+            for (int j = spread_to(i, C, M); j < spread_to(i + 1, C, M); ++j)
+                copy_one(C0 + j, to, k);
+        }
 #pragma unroll
         for (int a = 0; a < TN; ++a)
 #pragma unroll
             for (int b = 0; b < TM; ++b)
                 acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, d.w[a]),
                                                                   __builtin_bit_cast(i32x4, d.x[b]), acc[a][b], 0, 0, 0);
+        spread<M, R, C>();
     };
+    using C0 = std::integral_constant<int, 0>;
+    using CH = std::integral_constant<int, L / 2>;
+    using CL = std::integral_constant<int, L>;
     // Step s multiplies stage s. In its middle the wave waits for its copies of
     // stage s + 1 (those of s + 2 and s + 3 stay in flight) and meets the other
-    // waves: then stage s + 1 is whole, and stage s, all of whose reads are
-    // done, takes the copies of stage s + 4. The second half's fragments are in
-    // registers by then, so the matrix unit has work while the first half's of
-    // the next step are read.
+    // waves: then stage s + 1 is whole, and every wave has read all of stage
+    // s - 1, whose place takes stage s + 4: half of its copies go out in the
+    // second half of step s, half in the first half of step s + 1. Reads of
+    // stage s may still be on their way at the meeting; its place is not
+    // written before the next one. A step's second half has its fragments in
+    // registers (or about to be) when the first half of the next step's are read.
+    // Steps past the last multiply nothing: a stage past K is not copied, and
+    // its place is read (in bounds) but not used.
     const int steps = p.K / kStageK;                    // even
     Fr d0, d1;
-    copy(0);
-    copy(1);
-    if (steps > 2) {
-        copy(2);
-        copy(3);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        if (s < steps)
+            copy(s);
+    if (steps > 2)
         wait_barrier<3 * L>();
-    } else {
+    else
         wait_barrier<L>();
-    }
-    read(0, f0, d0);
+#pragma unroll
+    for (int j = 0; j < TN + TM; ++j)
+        read_one(j, s_dyn + f0, d0);
+    uint32_t cur = 0, to = 3 * kStageBytes, k = 3 * kStageK;    // stage s; the place and K of the stage being copied
+    auto after = [&](uint32_t at) { return at == (kStages - 1) * kStageBytes ? 0u : at + kStageBytes; };
     int s = 0;
-    for (; s + 4 < steps; ++s) {
-        read(s, f1, d1);
-        multiply(d0);
-        spread<TN * TM, TN + TM, 0>();
-        wait_barrier<2 * L>();
-        read(s + 1, f0, d0);
-        copy(s + 4);
-        multiply(d1);
-        spread<TN * TM, TN + TM, L>();
+    if (steps > 4) {
+        half_step(d0, d1, cur + f1, C0(), C0(), 0, 0);  // stage 3 is already on its way
+        for (;; ++s) {
+            wait_barrier<2 * L>();
+            to = after(to);
+            k += kStageK;
+            const uint32_t next = after(cur);
+            half_step(d1, d0, next + f0, C0(), CH(), to, k);
+            cur = next;
+            if (s + 5 >= steps)
+                break;
+            half_step(d0, d1, cur + f1, CH(), CL(), to, k);
+        }
+        // step s + 1 = steps - 4: the rest of the last stage's copies
+        half_step(d0, d1, cur + f1, CH(), CL(), to, k);
+        ++s;
+    } else {
+        half_step(d0, d1, cur + f1, C0(), C0(), 0, 0);
     }
-    for (; s < steps; ++s) {                            // the last four steps: nothing left to copy
-        read(s, f1, d1);
-        multiply(d0);
-        wait_barrier<0>();
+    for (;;) {                                          // nothing left to copy; the first half of step s is done
         if (s + 1 < steps)
-            read(s + 1, f0, d0);
-        multiply(d1);
+            wait_barrier<0>();
+        const uint32_t next = after(cur);
+        half_step(d1, d0, next + f0, C0(), C0(), 0, 0);
+        cur = next;
+        if (++s >= steps)
+            break;
+        half_step(d0, d1, cur + f1, C0(), C0(), 0, 0);
     }
 
-    // Epilogue: 32 tokens at a time through the wave's own part of LDS (all
-    // reads of the stages are done), so that a store writes whole runs of a row
+    // Epilogue: 32 tokens at a time through the wave's own part of LDS (past
+    // the barrier all reads of the stages are done), so that a store writes whole runs of a row
     // (16 TG or 32 TG lanes' worth) instead of 8 bytes per token.
     __syncthreads();
     constexpr int kElem = F32 ? 4 : 2;
