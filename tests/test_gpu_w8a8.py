@@ -45,7 +45,8 @@ def swiglu(c):
 
 DENSE = [(1, 16, 128), (1, 2064, 768), (3, 4096, 256), (15, 48, 1280), (16, 128, 2048), (17, 272, 128), (31, 4096, 4096),
          (33, 400, 896), (64, 256, 512), (65, 1040, 640), (100, 128, 7168), (129, 2064, 768), (256, 256, 128),
-         (257, 512, 384), (333, 2064, 768), (512, 768, 2048), (700, 1552, 1024), (1500, 2048, 256), (2049, 272, 1152)]
+         (257, 512, 384), (333, 2064, 768), (512, 768, 2048), (700, 1552, 1024), (1500, 2048, 256), (2049, 272, 1152), (4100, 4112, 256),
+         (3000, 4112, 384), (1, 4096, 14336), (30, 14336, 1152), (60, 16400, 256), (12, 14336, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -100,7 +101,9 @@ GROUPED = [  # T, E, local from, local, k, H, I, routing
     (16, 128, 0, 128, 8, 2048, 768, "uniform"), (33, 60, 15, 30, 4, 384, 256, "zipf"), (40, 4, 0, 4, 1, 640, 384, "one"),
     (64, 16, 0, 16, 2, 256, 128, "zipf"), (130, 8, 0, 8, 2, 512, 256, "one"), (300, 16, 0, 16, 4, 1024, 384, "zipf"),
     (513, 32, 8, 16, 8, 256, 640, "uniform"), (700, 3, 0, 3, 3, 384, 1024, "uniform"), (2048, 64, 0, 64, 2, 256, 128, "zipf"),
-    (50, 16, 12, 4, 2, 256, 256, "one"), (50, 16, 0, 4, 2, 256, 256, "one")]
+    (50, 16, 12, 4, 2, 256, 256, "one"), (50, 16, 0, 4, 2, 256, 256, "one"), (1024, 64, 0, 64, 8, 256, 768, "uniform"),
+    (600, 64, 0, 64, 8, 1792, 256, "zipf"), (4096, 4, 0, 4, 2, 2048, 1024, "uniform"), (200, 300, 0, 300, 3, 256, 256, "zipf"),
+    (3, 1024, 0, 1024, 16, 256, 128, "uniform")]
 
 
 @pytest.mark.parametrize("T,E,begin,L,k,H,I,mode", GROUPED)

@@ -7,6 +7,7 @@
 // MFMA: v_mfma_i32_16x16x64_i8, the weight rows as operand A and the tokens as
 // operand B, so that a result lane holds four consecutive outputs of one token.
 // Both operands take the same permutation of K, which leaves the sums as they are.
+#include <cmath>
 #include <mutex>
 
 #include "gemm_core.hpp"
@@ -33,6 +34,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 
 struct W8Args {
     const int8_t *a;
+    uint32_t a_bytes;
     const float *as;
     const int32_t *a_row_index;
     int top_k;
@@ -45,85 +47,192 @@ struct W8Args {
     int K, N;
 };
 
-// Activation row of result row r: what the index holds is kept inside the array.
-__device__ __forceinline__ int act_row(const W8Args &p, int r)
+// Activation row of result row r, in two steps: the index entry (0 where there
+// is no index; loaded first, ahead of what can go out without it), then the row,
+// kept inside the array whatever the entry holds.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t index_rsrc(const W8Args &p)
 {
-    if (!p.a_row_index)
-        return r;
-    const int i = p.a_row_index[r];
-    return (i < 0 ? 0 : (i < p.max_rows ? i : p.max_rows - 1)) / p.top_k;
+    return make_rsrc(p.a_row_index, p.a_row_index ? (uint32_t)p.max_rows * 4u : 0u);
 }
 
-// Chunk `chunk` of at most CS rows of one expert, found by one wave from the
-// row offsets: false past the last chunk. Every lane gets the result.
-__device__ __forceinline__ bool find_chunk(const W8Args &p, int CS, int chunk, int lane, int &e, int &r0, int &rows)
+__device__ __forceinline__ int load_index(__amdgpu_buffer_rsrc_t ri, int r)
 {
-    if (!p.offsets) {
-        e = 0;
-        r0 = chunk * CS;
-        rows = p.max_rows - r0;
-        rows = rows < CS ? rows : CS;
-        return rows > 0;
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, (uint32_t)r * 4u, 0, 0);
+}
+
+__device__ __forceinline__ int act_row(const W8Args &p, int r, int i)
+{
+    i = i < 0 ? 0 : (i < p.max_rows ? i : p.max_rows - 1);
+    return p.a_row_index ? i / p.top_k : r;
+}
+
+// The chunks (at most CS rows of one expert each) as one wave sees them, four
+// experts to a lane: expert 64 i + lane has n[i] chunks, the first of them
+// chunk first[i]. All offsets are loaded before the first is used; past 256
+// experts the rest is scanned in rounds of 256.
+constexpr int kScan = 4;
+
+struct Chunks {
+    int o0[kScan], o1[kScan], first[kScan], n[kScan];
+};
+
+// Experts e0 .. e0 + 255, whose first chunk is `before`; returns the next one's.
+__device__ __forceinline__ int scan_chunks(const W8Args &p, int CS, int lane, int e0, int before, Chunks &c)
+{
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+        const int e = e0 + 64 * i + lane, ee = e < p.E ? e : p.E - 1;
+        c.o0[i] = p.offsets[ee];
+        c.o1[i] = p.offsets[ee + 1];
     }
-    int before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const int ee = e0 + lane < p.E ? e0 + lane : p.E - 1;
-        const int o0 = p.offsets[ee], o1 = p.offsets[ee + 1];
-        const int n = e0 + lane < p.E ? (o1 - o0 + CS - 1) / CS : 0;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+        c.n[i] = e0 + 64 * i + lane < p.E ? (c.o1[i] - c.o0[i] + CS - 1) / CS : 0;
         int total;
-        const int first = before + wave_exclusive_scan(n, total);
-        const uint64_t at = __ballot(first <= chunk && chunk < first + n);
+        c.first[i] = before + wave_exclusive_scan(c.n[i], total);
+        before += total;
+    }
+    return before;
+}
+
+// Chunk `chunk`, where it is one of c's: its expert, first row and rows.
+__device__ __forceinline__ bool pick_chunk(const W8Args &p, int CS, int e0, int chunk, const Chunks &c, int &e, int &r0,
+                                           int &rows)
+{
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+        const uint64_t at = __ballot(c.first[i] <= chunk && chunk < c.first[i] + c.n[i]);
         if (at) {
             const int l = __builtin_ctzll(at);
-            e = e0 + l;
-            const int c = chunk - __builtin_amdgcn_readlane(first, l);
-            r0 = __builtin_amdgcn_readlane(o0, l) + c * CS;
-            const int end = __builtin_amdgcn_readlane(o1, l);
+            e = e0 + 64 * i + l;
+            r0 = __builtin_amdgcn_readlane(c.o0[i], l) + (chunk - __builtin_amdgcn_readlane(c.first[i], l)) * CS;
+            const int end = __builtin_amdgcn_readlane(c.o1[i], l);
             rows = (end < p.max_rows ? end : p.max_rows) - r0;
-            rows = rows < CS ? rows : CS;
-            return rows > 0 && r0 >= 0;
+            found = r0 >= 0 && rows > 0;
         }
-        before += total;
+    }
+    rows = rows < CS ? rows : CS;
+    return found;
+}
+
+__device__ __forceinline__ bool dense_chunk(const W8Args &p, int CS, int chunk, int &e, int &r0, int &rows)
+{
+    e = 0;
+    r0 = chunk * CS;
+    rows = p.max_rows - r0;
+    rows = rows < CS ? rows : CS;
+    return rows > 0;
+}
+
+// Chunk `chunk`: its expert, first row and rows; false past the last chunk. One
+// wave, every lane gets the result.
+__device__ __forceinline__ bool find_chunk(const W8Args &p, int CS, int chunk, int lane, int &e, int &r0, int &rows)
+{
+    if (!p.offsets)
+        return dense_chunk(p, CS, chunk, e, r0, rows);
+    e = r0 = rows = 0;
+    for (int e0 = 0, before = 0; e0 < p.E; e0 += 64 * kScan) {
+        Chunks c;
+        before = scan_chunks(p, CS, lane, e0, before, c);
+        if (chunk < before)
+            return pick_chunk(p, CS, e0, chunk, c, e, r0, rows);
     }
     return false;
 }
 
-// Few rows per expert: each wave streams its own weight rows from memory to
-// registers and multiplies them with NSUB subtiles of 16 tokens; no LDS, no
-// barrier. The weights are what such a call has to read, once.
-template <int KIND, bool F32, int NSUB, int TPW>
-__global__ __launch_bounds__(256) void w8_stream_kernel(W8Args p, int blocks)
+// Tile (chunk of rows, column tile) of linear index i: the column tiles of
+// groups of eight chunks, so that the workgroups running at one time share both
+// operands.
+__device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
+{
+    constexpr int G = 8;
+    const int g = i / (G * tn), rest = i - g * G * tn;
+    const int gm = tm - g * G < G ? tm - g * G : G;
+    m = g * G + rest % gm;
+    n = rest / gm;
+}
+
+// Workgroup b's tile of the tiles that there are (the grid holds as many as
+// there can be): XCD x (workgroups x, x + 8, ...) takes the x-th share of them,
+// so that those which share operands also share an L2. False where b has none.
+__device__ __forceinline__ bool find_tile(const W8Args &p, int CS, int tn, int b, int lane, int &e, int &r0, int &rows,
+                                          int &nt)
+{
+    Chunks c;
+    int tm = 0;
+    if (!p.offsets)
+        tm = (p.max_rows + CS - 1) / CS;
+    else
+        for (int e0 = 0; e0 < p.E; e0 += 64 * kScan)
+            tm = scan_chunks(p, CS, lane, e0, tm, c);
+    const int total = tm * tn, per = total / kXcds, extra = total % kXcds;
+    const int x = b % kXcds, ix = b / kXcds;
+    if (ix >= per + (x < extra ? 1 : 0))
+        return false;
+    int mt;
+    tile_of(x * per + (x < extra ? x : extra) + ix, tm, tn, mt, nt);
+    if (!p.offsets)
+        return dense_chunk(p, CS, mt, e, r0, rows);
+    e = r0 = rows = 0;
+    if (p.E <= 64 * kScan)
+        return pick_chunk(p, CS, 0, mt, c, e, r0, rows);
+    return find_chunk(p, CS, mt, lane, e, r0, rows);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per expert: the weights are what such a call has to read, once. Each
+// wave streams its own weight rows from memory to registers, RING groups of 128
+// bytes of K ahead, and multiplies them with NSUB subtiles of 16 tokens, whose
+// rows it fetches the same way (they stay in the caches). WK waves of a
+// workgroup share a set of rows, each with its part of K, and add their sums
+// (integers, so in any order) through LDS; else no LDS and no barrier. The
+// weights are read once, non-temporally.
+// ---------------------------------------------------------------------------
+template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING>
+__global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
 {
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
     constexpr int TG = SW ? TPW / 2 : TPW;              // tiles side by side: a lane's outputs are 4 TG consecutive ones
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int WN = 4 / WK;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int m = lane & 15, q = lane >> 4;
+    const int wn = wave / WK, wk = wave % WK;
     const int chunk = blockIdx.x / blocks;
     const int block = blockIdx.x - chunk * blocks;
     int e, r0, rows;
     if (!find_chunk(p, 16 * NSUB, chunk, lane, e, r0, rows))
         return;
+    e = uniform(e);
     const int cols = SW ? p.N / 2 : p.N;                // outputs per row
-    const int n0 = (block * 4 + wave) * 16 * TG;
-    if (n0 >= cols)
+    const int n0 = (block * WN + wn) * 16 * TG;
+    if (WK == 1 && n0 >= cols)
         return;
     // weight row of lane row m in tile t: outputs n0 + (m / 4) 4 TG + 4 t + m % 4 (gate), the same + N / 2 (up)
-    const int8_t *wrow[TPW];
+    uint32_t wo[TPW], xo[NSUB];
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
         int n = n0 + (m >> 2) * 4 * TG + (t % TG) * 4 + (m & 3);
         n = n < cols ? n : cols - 1;
         if (SW && t >= TG)
             n += cols;
-        wrow[t] = p.wq + ((size_t)e * p.N + n) * p.K + q * 32;
+        wo[t] = (uint32_t)n * p.K + q * 16;
     }
-    const int8_t *xrow[NSUB];
-    int arow[NSUB];
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * p.K, (uint32_t)p.N * p.K);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, p.a_bytes), ri = index_rsrc(p);
+    // what the rows and the epilogue need sets out first
+    const int nq = n0 + q * 4 * TG;
+    int row[NSUB], idx[NSUB];
 #pragma unroll
     for (int s = 0; s < NSUB; ++s) {
-        const int r = r0 + (16 * s + m < rows ? 16 * s + m : rows - 1);
-        arow[s] = act_row(p, r);
-        xrow[s] = p.a + (size_t)arow[s] * p.K + q * 32;
+        row[s] = r0 + (16 * s + m < rows ? 16 * s + m : rows - 1);
+        idx[s] = load_index(ri, row[s]);
+    }
+    floatx4 ws[TPW];
+#pragma unroll
+    for (int t = 0; t < TPW; ++t) {
+        const int n = nq + 4 * (t % TG);
+        ws[t] = *reinterpret_cast<const floatx4 *>(p.ws + (size_t)e * p.N + (n < cols ? n : cols - 4) + (SW && t >= TG ? cols : 0));
     }
     i32x4 acc[NSUB][TPW];
 #pragma unroll
@@ -131,32 +240,94 @@ __global__ __launch_bounds__(256) void w8_stream_kernel(W8Args p, int blocks)
 #pragma unroll
         for (int t = 0; t < TPW; ++t)
             acc[s][t] = i32x4{0, 0, 0, 0};
-    for (int k = 0; k < p.K; k += 128) {
-        u32x4 w[TPW][2], x[NSUB][2];
+    u32x4 w[RING][TPW][2], x[RING][NSUB][2];
+    auto load_w = [&](int j, uint32_t k) {
 #pragma unroll
         for (int t = 0; t < TPW; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w[t][h] = *reinterpret_cast<const u32x4 *>(wrow[t] + k + 16 * h);
+                w[j][t][h] = bload16_codes<true>(rw, wo[t] + 64 * h, k);
+    };
+    auto load_x = [&](int j, uint32_t k) {
 #pragma unroll
         for (int s = 0; s < NSUB; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                x[s][h] = *reinterpret_cast<const u32x4 *>(xrow[s] + k + 16 * h);
+                x[j][s][h] = bload16(rx, xo[s] + 64 * h, k);
+    };
+    auto multiply = [&](int j) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < NSUB; ++s)
 #pragma unroll
                 for (int t = 0; t < TPW; ++t)
-                    acc[s][t] = mfma_i8(w[t][h], x[s][h], acc[s][t]);
+                    acc[s][t] = mfma_i8(w[j][t][h], x[j][s][h], acc[s][t]);
+    };
+    // groups [g, end) of this wave, in rounds of RING: while a round is multiplied the next one is on its way
+    const int G = p.K / 128, end = (wk + 1) * G / WK;
+    int g = wk * G / WK;
+    float as[NSUB];
+    auto find_rows = [&]() {
+#pragma unroll
+        for (int s = 0; s < NSUB; ++s) {
+            const int ar = act_row(p, row[s], idx[s]);
+            xo[s] = (uint32_t)ar * p.K + q * 16;
+            as[s] = p.as[ar];
+        }
+    };
+    if (end - g >= RING) {
+        // the first round's weights set out before the tokens' rows are known
+#pragma unroll
+        for (int j = 0; j < RING; ++j)
+            load_w(j, (uint32_t)(g + j) * 128);
+        __builtin_amdgcn_sched_barrier(0);
+        find_rows();
+#pragma unroll
+        for (int j = 0; j < RING; ++j)
+            load_x(j, (uint32_t)(g + j) * 128);
+        for (; end - g >= 2 * RING; g += RING)
+#pragma unroll
+            for (int j = 0; j < RING; ++j) {
+                multiply(j);
+                load_w(j, (uint32_t)(g + RING + j) * 128);
+                load_x(j, (uint32_t)(g + RING + j) * 128);
+            }
+#pragma unroll
+        for (int j = 0; j < RING; ++j)
+            multiply(j);
+        g += RING;
+    } else {
+        find_rows();
     }
-    const int nq = n0 + q * 4 * TG;
+    for (; g < end; ++g) {
+        load_w(0, (uint32_t)g * 128);
+        load_x(0, (uint32_t)g * 128);
+        multiply(0);
+    }
+    if constexpr (WK > 1) {
+        __shared__ i32x4 s_part[WN][WK - 1][NSUB * TPW][64];
+#pragma unroll
+        for (int s = 0; s < NSUB; ++s)
+#pragma unroll
+            for (int t = 0; t < TPW; ++t)
+                if (wk > 0)
+                    s_part[wn][wk - 1][s * TPW + t][lane] = acc[s][t];
+        __syncthreads();
+        if (wk > 0)
+            return;
+#pragma unroll
+        for (int i = 0; i < WK - 1; ++i)
+#pragma unroll
+            for (int s = 0; s < NSUB; ++s)
+#pragma unroll
+                for (int t = 0; t < TPW; ++t)
+                    acc[s][t] += s_part[wn][i][s * TPW + t][lane];
+    }
 #pragma unroll
     for (int s = 0; s < NSUB; ++s) {
         if (16 * s + m >= rows)
             continue;
-        const float as = p.as[arow[s]];
         const size_t crow = (size_t)(r0 + 16 * s + m) * cols;
 #pragma unroll
         for (int t = 0; t < TG; ++t) {
@@ -166,40 +337,43 @@ __global__ __launch_bounds__(256) void w8_stream_kernel(W8Args p, int blocks)
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float *ws = p.ws + (size_t)e * p.N + n + i;
-                v[i] = (float)acc[s][t][i] * as * ws[0];
+                v[i] = (float)acc[s][t][i] * as[s] * ws[t][i];
                 if constexpr (SW)
-                    v[i] = silu_fast(v[i]) * ((float)acc[s][t + TG][i] * as * ws[cols]);
+                    v[i] = silu_fast(v[i]) * ((float)acc[s][t + TG][i] * as[s] * ws[t + TG][i]);
             }
             if constexpr (F32)
                 *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + crow + n) = floatx4{v[0], v[1], v[2], v[3]};
             else
                 *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + crow + n) =
-                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         }
     }
 }
 
-template <int KIND, bool F32>
+// At most this many chunks of CS rows: the full ones and one part-filled per expert with rows.
+long long chunks_at_most(const W8GemmLaunch &g, int CS)
+{
+    if (!g.offsets)
+        return (g.max_rows + CS - 1) / CS;
+    return (long long)g.max_rows / CS + (g.num_experts < g.max_rows ? g.num_experts : g.max_rows);
+}
+
+template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING>
 hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 {
-    constexpr int TPW = 4, NSUB = 2;
     constexpr int TG = KIND == MOE_GEMM_W13_SWIGLU ? TPW / 2 : TPW;
     const int cols = KIND == MOE_GEMM_W13_SWIGLU ? g.N / 2 : g.N;
-    const int blocks = (cols + 64 * TG - 1) / (64 * TG);
-    // at most one part-filled chunk per expert with rows, and the full ones
-    const int full = g.max_rows / (16 * NSUB);
-    const long long chunks = g.offsets ? (long long)full + (g.num_experts < g.max_rows ? g.num_experts : g.max_rows)
-                                       : (g.max_rows + 16 * NSUB - 1) / (16 * NSUB);
-    hipLaunchKernelGGL((w8_stream_kernel<KIND, F32, NSUB, TPW>), dim3((unsigned)(chunks * blocks)), dim3(256), 0, st, p,
-                       blocks);
+    constexpr int BC = 16 * TG * (4 / WK);
+    const int blocks = (cols + BC - 1) / BC;
+    hipLaunchKernelGGL((w8_stream_kernel<KIND, F32, NSUB, TPW, WK, RING>),
+                       dim3((unsigned)(chunks_at_most(g, 16 * NSUB) * blocks)), dim3(256), 0, st, p, blocks);
     return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Many rows per expert: a workgroup of four waves computes BN weight rows x BM
 // tokens, a wave 32 TN x 32 TM of them with v_mfma_i32_32x32x32_i8. Both
-// operands pass through LDS, kStageK bytes of K to a stage, five stages deep.
+// operands pass through LDS, kStageK bytes of K to a stage, NS stages deep.
 //
 // A stage holds BN + BM rows of 64 bytes, four 16-byte chunks each; row r keeps
 // chunk c at place c ^ ((r >> 2) & 3), so that the 64 lanes of a fragment read
@@ -213,7 +387,6 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // wave's columns, which makes a lane's sixteen results of a tile consecutive.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 64;
-constexpr int kStages = 5;
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) unsigned char lds_byte;
@@ -230,25 +403,34 @@ __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, lds_byte *dst, 
 }
 
 template <int N>
-__device__ __forceinline__ void wait_barrier()
+__device__ __forceinline__ void wait_for()
 {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(N));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The wait of an early step f < NS - 3, while copies that went out weights first
+// are still on their way: the tokens' of NS - 3 - f stages, and f whole stages.
+template <int NS, int LM, int L>
+__device__ __forceinline__ void early_wait(int f)
+{
+    if (f == 0)
+        wait_for<(NS - 3) * LM>();
+    else if (f == 1)
+        wait_for<(NS > 4 ? NS - 4 : 0) * LM + L>();
+    else
+        wait_for<(NS > 5 ? NS - 5 : 0) * LM + 2 * L>();
+}
+
+template <int N>
+__device__ __forceinline__ void wait_barrier()
+{
+    wait_for<N>();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
-}
-
-// Tile (row tile, column tile) of linear index i: column tiles in groups of
-// eight row tiles, so that the workgroups running at one time share both operands.
-__device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
-{
-    constexpr int G = 8;
-    const int g = i / (G * tn), rest = i - g * G * tn;
-    const int gm = tm - g * G < G ? tm - g * G : G;
-    m = g * G + rest % gm;
-    n = rest / gm;
 }
 
 // How many of n things spread evenly over m places come before place i.
@@ -277,8 +459,8 @@ struct Frags {
     u32x4 w[TN], x[TM];
 };
 
-template <int KIND, bool F32, int TN, int TM, int NWN, int NWM>
-__global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int tn)
+template <int KIND, bool F32, int TN, int TM, int NWN, int NWM, int NS>
+__global__ __launch_bounds__(256, TN * TM > 8 ? 1 : 2) void w8_tile_kernel(W8Args p, int tn)
 {
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
     constexpr int TG = SW ? TN / 2 : TN;
@@ -290,14 +472,8 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
     extern __shared__ __align__(16) unsigned char s_dyn[];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wn = wave / NWM, wm = wave % NWM;
-    // XCD x (workgroups x, x + 8, ...) takes the x-th share of the tiles
-    const int total = gridDim.x, per = total / kXcds, extra = total % kXcds;
-    const int x = blockIdx.x % kXcds;
-    const int item = x * per + (x < extra ? x : extra) + blockIdx.x / kXcds;
-    int mt, nt;
-    tile_of(item, tm, tn, mt, nt);
-    int e, r0, rows;
-    if (!find_chunk(p, BM, mt, lane, e, r0, rows))
+    int e, r0, rows, nt;
+    if (!find_tile(p, BM, tn, blockIdx.x, lane, e, r0, rows, nt))
         return;
     e = uniform(e);
     const int cols = SW ? p.N / 2 : p.N;
@@ -307,23 +483,10 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
     // this lane's place in a copy of 16 rows, and the chunk that belongs there
     const int prow = lane >> 2;
     auto chunk_at = [&](int row) { return (uint32_t)(((lane & 3) ^ ((row >> 2) & 3)) * 16); };
-    uint32_t wo[LN], xo[LM];
-#pragma unroll
-    for (int j = 0; j < LN; ++j) {
-        const int row = (wave * LN + j) * 16 + prow;    // row of the stage: wave's columns, tile, row of the tile
-        const int w = row / (32 * TN), t = row / 32 % TN, r = row % 32;
-        int n = n0 + w * 32 * TG + ((r >> 2) & 1) * 16 * TG + (t % TG) * 16 + (r >> 3) * 4 + (r & 3);
-        n = n < cols ? n : cols - 1;
-        wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + chunk_at(row);
-    }
-#pragma unroll
-    for (int j = 0; j < LM; ++j) {
-        const int row = (wave * LM + j) * 16 + prow;
-        xo[j] = (uint32_t)act_row(p, r0 + (row < rows ? row : rows - 1)) * K + chunk_at(row);
-    }
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * K, (uint32_t)p.N * K);
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, 0xFFFFFFFFu);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, p.a_bytes), ri = index_rsrc(p);
     lds_byte *lds = (lds_byte *)s_dyn;
+    uint32_t wo[LN], xo[LM];
     // one of a wave's L copies of a stage: K bytes [k, k + 64) to the stage at byte `at` of LDS
     auto copy_one = [&](int j, uint32_t at, uint32_t k) {
         lds_byte *dst = lds + at;
@@ -332,11 +495,72 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
         else
             copy16(rx, dst + BN * kStageK + (wave * LM + j - LN) * 1024, xo[j < LN ? 0 : j - LN], k);
     };
-    auto copy = [&](int s) {
+    // copies [j0, j1) of the first NS - 1 stages (past K: the last one again, which is never read)
+    const int steps = p.K / kStageK;                    // even
+    auto first_copies = [&](auto j0, auto j1) {
 #pragma unroll
-        for (int j = 0; j < L; ++j)
-            copy_one(j, (uint32_t)(s % kStages) * kStageBytes, (uint32_t)s * kStageK);
+        for (int s = 0; s < NS - 1; ++s)
+#pragma unroll
+            for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
+                copy_one(j, s * kStageBytes, (uint32_t)(s < steps ? s : steps - 1) * kStageK);
     };
+    using C0 = std::integral_constant<int, 0>;
+    using CN = std::integral_constant<int, LN>;
+    using CH = std::integral_constant<int, L / 2>;
+    using CL = std::integral_constant<int, L>;
+    // what the tokens' rows and the epilogue need sets out first: index entries
+    // of the rows to copy and of the lane's result rows, the columns' scales
+    const int half = lane >> 5, m32 = lane & 31;
+    int xrow[LM], xidx[LM], crow[TM], cidx[TM];
+#pragma unroll
+    for (int j = 0; j < LM; ++j) {
+        const int row = (wave * LM + j) * 16 + prow;
+        xrow[j] = r0 + (row < rows ? row : rows - 1);
+        xidx[j] = load_index(ri, xrow[j]);
+    }
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int m = (wm * TM + b) * 32 + m32;
+        crow[b] = r0 + (m < rows ? m : rows - 1);
+        cidx[b] = load_index(ri, crow[b]);
+    }
+    const int nw = n0 + wn * 32 * TG;                   // the wave's first column
+    float wsv[TN][16];
+    auto load_scales = [&]() {
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                int n = nw + half * 16 * TG + (t % TG) * 16 + g * 4;
+                n = (n < cols ? n : cols - 4) + (SW && t >= TG ? cols : 0);
+                const floatx4 v = *reinterpret_cast<const floatx4 *>(p.ws + (size_t)e * p.N + n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    wsv[t][4 * g + i] = v[i];
+            }
+    };
+    constexpr bool kScalesFirst = TN * TM <= 8;         // the largest tile has no registers left for them
+    if constexpr (kScalesFirst)
+        load_scales();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < LN; ++j) {
+        const int row = (wave * LN + j) * 16 + prow;    // row of the stage: wave's columns, tile, row of the tile
+        const int w = row / (32 * TN), t = row / 32 % TN, r = row % 32;
+        int n = n0 + w * 32 * TG + ((r >> 2) & 1) * 16 * TG + (t % TG) * 16 + (r >> 3) * 4 + (r & 3);
+        n = n < cols ? n : cols - 1;
+        wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + chunk_at(row);
+    }
+    // the weights set out before the tokens' rows are known
+    first_copies(C0(), CN());
+    __builtin_amdgcn_sched_barrier(0);
+    float asv[TM];
+#pragma unroll
+    for (int b = 0; b < TM; ++b)
+        asv[b] = p.as[act_row(p, crow[b], cidx[b])];
+#pragma unroll
+    for (int j = 0; j < LM; ++j)
+        xo[j] = (uint32_t)act_row(p, xrow[j], xidx[j]) * K + chunk_at((wave * LM + j) * 16 + prow);
     // fragment reads: lane l holds chunk 2 kk + l / 32 of row l % 32
     const int fr = lane & 31;
     const uint32_t f0 = (uint32_t)(fr * 64 + (((lane >> 5) ^ ((fr >> 2) & 3)) * 16));
@@ -379,49 +603,46 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
                                                                   __builtin_bit_cast(i32x4, d.x[b]), acc[a][b], 0, 0, 0);
         spread<M, R, C>();
     };
-    using C0 = std::integral_constant<int, 0>;
-    using CH = std::integral_constant<int, L / 2>;
-    using CL = std::integral_constant<int, L>;
     // Step s multiplies stage s. In its middle the wave waits for its copies of
-    // stage s + 1 (those of s + 2 and s + 3 stay in flight) and meets the other
+    // stage s + 1 (those of the NS - 3 after it stay in flight) and meets the other
     // waves: then stage s + 1 is whole, and every wave has read all of stage
-    // s - 1, whose place takes stage s + 4: half of its copies go out in the
+    // s - 1, whose place takes stage s + NS - 1: half of its copies go out in the
     // second half of step s, half in the first half of step s + 1. Reads of
     // stage s may still be on their way at the meeting; its place is not
     // written before the next one. A step's second half has its fragments in
     // registers (or about to be) when the first half of the next step's are read.
     // Steps past the last multiply nothing: a stage past K is not copied, and
     // its place is read (in bounds) but not used.
-    const int steps = p.K / kStageK;                    // even
+    // (The first stages' copies went out weights first: until their tokens
+    // are in, fewer may stay in flight.)
     Fr d0, d1;
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-        if (s < steps)
-            copy(s);
-    if (steps > 2)
-        wait_barrier<3 * L>();
-    else
-        wait_barrier<L>();
+    __builtin_amdgcn_sched_barrier(0);
+    first_copies(CN(), CL());
+    wait_barrier<(NS - 2) * LM>();
 #pragma unroll
     for (int j = 0; j < TN + TM; ++j)
         read_one(j, s_dyn + f0, d0);
-    uint32_t cur = 0, to = 3 * kStageBytes, k = 3 * kStageK;    // stage s; the place and K of the stage being copied
-    auto after = [&](uint32_t at) { return at == (kStages - 1) * kStageBytes ? 0u : at + kStageBytes; };
+    uint32_t cur = 0, to = (NS - 2) * kStageBytes, k = (NS - 2) * kStageK;    // stage s; the place and K of the stage being copied
+    auto after = [&](uint32_t at) { return at == (NS - 1) * kStageBytes ? 0u : at + kStageBytes; };
     int s = 0;
-    if (steps > 4) {
-        half_step(d0, d1, cur + f1, C0(), C0(), 0, 0);  // stage 3 is already on its way
+    if (steps > NS - 1) {
+        half_step(d0, d1, cur + f1, C0(), C0(), 0, 0);  // stage NS - 2 is already on its way
         for (;; ++s) {
-            wait_barrier<2 * L>();
+#pragma unroll
+            for (int f = 0; f < NS - 3; ++f)
+                if (s == f)
+                    early_wait<NS, LM, L>(f);
+            wait_barrier<(NS - 3) * L>();
             to = after(to);
             k += kStageK;
             const uint32_t next = after(cur);
             half_step(d1, d0, next + f0, C0(), CH(), to, k);
             cur = next;
-            if (s + 5 >= steps)
+            if (s + NS >= steps)
                 break;
             half_step(d0, d1, cur + f1, CH(), CL(), to, k);
         }
-        // step s + 1 = steps - 4: the rest of the last stage's copies
+        // step s + 1 = steps - (NS - 1): the rest of the last stage's copies
         half_step(d0, d1, cur + f1, CH(), CL(), to, k);
         ++s;
     } else {
@@ -441,35 +662,21 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
     // Epilogue: 32 tokens at a time through the wave's own part of LDS (past
     // the barrier all reads of the stages are done), so that a store writes whole runs of a row
     // (16 TG or 32 TG lanes' worth) instead of 8 bytes per token.
+    if constexpr (!kScalesFirst)
+        load_scales();
     __syncthreads();
     constexpr int kElem = F32 ? 4 : 2;
     constexpr int kRow = 32 * TG * kElem;               // bytes of a row in the wave's columns
     constexpr int kPitch = kRow + 16;
     constexpr int kLanes = kRow / 16;                   // lanes that store a row
-    static_assert(32 * kPitch * 4 <= kStageBytes * kStages, "the epilogue's rows fit the stages");
+    static_assert(32 * kPitch * 4 <= kStageBytes * NS, "the epilogue's rows fit the stages");
     unsigned char *buf = s_dyn + wave * (32 * kPitch);
-    const int half = lane >> 5, m32 = lane & 31;
-    const int nw = n0 + wn * 32 * TG;                   // the wave's first column
-    const float *wsp = p.ws + (size_t)e * p.N;
-    float wsv[TN][16];
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            int n = nw + half * 16 * TG + (t % TG) * 16 + g * 4;
-            n = (n < cols ? n : cols - 4) + (SW && t >= TG ? cols : 0);
-            const floatx4 v = *reinterpret_cast<const floatx4 *>(wsp + n);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                wsv[t][4 * g + i] = v[i];
-        }
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
         const int mb = (wm * TM + b) * 32;
         if (mb >= rows)
             break;
-        const int m = mb + m32;
-        const float as = p.as[act_row(p, r0 + (m < rows ? m : rows - 1))];
+        const float as = asv[b];
 #pragma unroll
         for (int t = 0; t < TG; ++t) {
             float v[16];
@@ -506,48 +713,92 @@ __global__ __launch_bounds__(256, 1) void w8_tile_kernel(W8Args p, int tm, int t
     }
 }
 
-template <int KIND, bool F32, int TN, int TM, int NWN, int NWM>
+template <int KIND, bool F32, int TN, int TM, int NWN, int NWM, int NS>
 void allow_lds(int bytes)
 {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM, NS>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int KIND, bool F32, int TN, int TM, int NWN, int NWM>
+template <int KIND, bool F32, int TN, int TM, int NWN, int NWM, int NS>
 hipError_t launch_tile(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 {
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
     constexpr int BN = 32 * TN * NWN, BM = 32 * TM * NWM, BC = SW ? BN / 2 : BN;
-    constexpr int lds = (BN + BM) * kStageK * kStages;
+    constexpr int lds = (BN + BM) * kStageK * NS;      // 256 x 256: all of a CU's; 128 x 128: two workgroups to a CU
     const int cols = SW ? g.N / 2 : g.N;
     const int tn = (cols + BC - 1) / BC;
-    const int tm = g.offsets ? g.max_rows / BM + (g.num_experts < g.max_rows ? g.num_experts : g.max_rows)
-                             : (g.max_rows + BM - 1) / BM;
+    const long long tm = chunks_at_most(g, BM);
     static std::once_flag once;
-    std::call_once(once, allow_lds<KIND, F32, TN, TM, NWN, NWM>, lds);
-    hipLaunchKernelGGL((w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM>), dim3((unsigned)(tm * tn)), dim3(256), lds, st, p,
-                       tm, tn);
+    std::call_once(once, allow_lds<KIND, F32, TN, TM, NWN, NWM, NS>, lds);
+    hipLaunchKernelGGL((w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM, NS>), dim3((unsigned)(tm * tn)), dim3(256), lds, st, p,
+                       tn);
     return hipGetLastError();
+}
+
+// Which kernel, from the expected rows per expert with rows, R', and the tiles
+// (items) that each would have; us on MI355X, weights read from HBM:
+//   few items, R' <= 32: the streaming kernel, K split over the waves, since 128 x 64 tiles
+//     leave CUs idle: dense 16 x 14336 x 4096 16.5 against 23.0, 1 x 4096 x 4096 8.2 against 13.0,
+//     32 x 4096 x 4096 11.8 against 14.0
+//   R' up to 40 (spread over the experts; 64 where it is exact): 64-row tiles; 256 columns of
+//     weights once that fills two workgroups per CU (128 experts 2048 -> 2 x 768: 64 tokens 71.3
+//     against 72.7 with 128, 256 tokens 74.5 against 79.8, 256 x 128 tiles 80.9)
+//   above: 128-row tiles, 256 columns where that fills the GPU (32 experts 7168 -> 2 x 2048, 64 rows
+//     each: 190 against 204 with 128 and 266 with 64 rows), else 128 (dense 256 x 14336 x 4096 30
+//     against 42), and 64 rows again where even those leave CUs idle (333 x 2064 x 768: 5.9
+//     against 7.1)
+//   256 x 256 where it gives nearly every CU a tile (4096 x 4096 x 7168: 118 against 152)
+template <int KIND, bool F32>
+hipError_t launch_kind(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
+{
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    const double R = g.expected_rows < 1 ? 1.0 : (double)g.expected_rows;
+    const double reached = g.offsets ? g.num_experts * (1.0 - pow(1.0 - 1.0 / g.num_experts, R)) : 1.0;
+    const double per = R / reached;
+    const int cols = SW ? g.N / 2 : g.N;
+    auto items = [&](int BN, int BM) {
+        const int BC = SW ? BN / 2 : BN;
+        return reached * ceil(per / BM) * ((cols + BC - 1) / BC);
+    };
+#ifdef CFG
+    return CFG(g, p, st);
+#endif
+    if (per <= 32.0 && items(128, 64) < 256.0) {
+        // a wave's tiles: as many as still give most CUs a workgroup
+        const bool few4 = items(64, 64) < 192.0, few2 = items(32, 64) < 192.0;
+        if (per <= 16.0) {
+            if (!few4)
+                return launch_stream<KIND, F32, 1, 4, 4, 2>(g, p, st);
+            if constexpr (!SW)
+                if (few2)
+                    return launch_stream<KIND, F32, 1, 1, 4, 4>(g, p, st);
+            return launch_stream<KIND, F32, 1, 2, 4, 4>(g, p, st);
+        }
+        return few4 ? launch_stream<KIND, F32, 2, 2, 4, 2>(g, p, st) : launch_stream<KIND, F32, 2, 4, 4, 2>(g, p, st);
+    }
+    if (per <= (g.offsets ? 40.0 : 64.0))
+        return items(256, 64) >= 384.0 ? launch_tile<KIND, F32, 2, 2, 4, 1, 4>(g, p, st)
+                                       : launch_tile<KIND, F32, 2, 1, 2, 2, 5>(g, p, st);
+    if (per >= 256.0 && items(256, 256) >= 240.0)
+        return launch_tile<KIND, F32, 4, 4, 2, 2, 5>(g, p, st);
+    if (items(256, 128) >= 384.0)
+        return launch_tile<KIND, F32, 4, 2, 2, 2, 3>(g, p, st);
+    return items(128, 128) >= 128.0 ? launch_tile<KIND, F32, 2, 2, 2, 2, 5>(g, p, st)
+                                    : launch_tile<KIND, F32, 2, 1, 2, 2, 5>(g, p, st);
 }
 
 }  // namespace
 
 hipError_t launch_w8_gemm(const W8GemmLaunch &g, hipStream_t st)
 {
-    const W8Args p{g.a, g.as, g.a_row_index, g.top_k, g.offsets, g.max_rows, g.num_experts, g.wq, g.ws, g.c, g.K, g.N};
-    const int per_expert = g.expected_rows / (g.num_experts > 0 ? g.num_experts : 1);
-    if (per_expert > 64) {
-        if (g.kind == MOE_GEMM_W13_SWIGLU)
-            return launch_tile<MOE_GEMM_W13_SWIGLU, false, 4, 4, 2, 2>(g, p, st);
-        if (g.c_f32)
-            return launch_tile<MOE_GEMM_W2, true, 4, 4, 2, 2>(g, p, st);
-        return launch_tile<MOE_GEMM_W2, false, 4, 4, 2, 2>(g, p, st);
-    }
+    const W8Args p{g.a, (uint32_t)((size_t)(g.a_row_index ? g.max_rows / g.top_k : g.max_rows) * g.K), g.as, g.a_row_index,
+                   g.top_k, g.offsets, g.max_rows, g.num_experts, g.wq, g.ws, g.c, g.K, g.N};
     if (g.kind == MOE_GEMM_W13_SWIGLU)
-        return launch_stream<MOE_GEMM_W13_SWIGLU, false>(g, p, st);
+        return launch_kind<MOE_GEMM_W13_SWIGLU, false>(g, p, st);
     if (g.c_f32)
-        return launch_stream<MOE_GEMM_W2, true>(g, p, st);
-    return launch_stream<MOE_GEMM_W2, false>(g, p, st);
+        return launch_kind<MOE_GEMM_W2, true>(g, p, st);
+    return launch_kind<MOE_GEMM_W2, false>(g, p, st);
 }
 
 }  // namespace moe

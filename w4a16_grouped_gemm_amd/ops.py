@@ -12,6 +12,7 @@ raise ValueError, a failed launch raises RuntimeError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -572,48 +573,56 @@ def moe_w4a4_forward(x: torch.Tensor, router_logits: torch.Tensor, w13_q: torch.
 # makes such rows; routing on scores
 # ---------------------------------------------------------------------------
 
-class _launch_on:
-    """Where a call runs: on `stream`, else on the current stream of the tensors' device. Inside, that device and
-    stream are current, so what the call allocates belongs to the stream that writes it."""
-
-    def __init__(self, device, stream):
-        self.guards = []
-        if stream is None:
-            if device.index != torch.cuda.current_device():
-                self.guards.append(torch.cuda.device(device))
-        elif isinstance(stream, torch.cuda.Stream):
-            self.guards.append(torch.cuda.stream(stream))
-        else:
-            self.guards.append(torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device)))
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
-        return False
+def _elsewhere(index: int, stream):
+    """None where a call on device `index` runs on the current stream of the current device, else a context in which
+    the device and the stream are current: what the call allocates inside then belongs to the stream that writes it."""
+    if stream is None:
+        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    return torch.cuda.stream(stream)
 
 
-def _need_all(device, *tensors):
-    """(tensor, dtype, shape, name): dtype, contiguity, device and shape; None entries are skipped."""
-    for t, dtype, shape, name in tensors:
-        if t is None:
-            continue
+def _expect(t, dtype, index, shape, name):
+    """t is a contiguous tensor of this dtype and shape on device `index` (one test where all is well: these calls
+    take a few microseconds in all)."""
+    if (t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous()):
         _need(t, dtype, name)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _out_dtype(out, out_dtype):
-    dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(out_dtype if out is None else out.dtype)
-    if dt is None:
-        raise ValueError("out dtype must be bfloat16 or float32")
-    return dt
+def _on_gpu(t, name) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
+
+
+def _out_dtype(dtype):
+    if dtype is torch.bfloat16:
+        return MOE_BF16
+    if dtype is torch.float32:
+        return MOE_F32
+    raise ValueError("out dtype must be bfloat16 or float32")
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape_ref(*args):
+    return ctypes.byref(make_shape(*args))
+
+
+@functools.lru_cache(maxsize=256)
+def _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale):
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return ctypes.byref(Router(int(score == "sigmoid"), int(num_groups), int(topk_groups), int(group_top),
+                               int(bool(renormalize)), float(scale)))
+
+
+# The current stream's handle without a Stream object around it (0.1 us instead of 2.7)
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None = None, score: str = "sigmoid",
@@ -624,37 +633,47 @@ def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None 
     score: "sigmoid" or "softmax" (over all experts). bias [E] is added for the selection only. With num_groups > 1
     only the experts of the topk_groups best groups are chosen from (a group's score: its best expert, or the sum of
     its two best with group_top=2). Weights are the scores, divided by their sum (renormalize), times scale."""
+    index = _on_gpu(logits, "logits")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return route_scored(logits, top_k, bias=bias, score=score, num_groups=num_groups, topk_groups=topk_groups,
+                                group_top=group_top, renormalize=renormalize, scale=scale)
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    _need_all(logits.device, (logits, torch.float32, (T, E), "logits"), (bias, torch.float32, (E,), "bias"))
-    if score not in ("softmax", "sigmoid"):
-        raise ValueError("score must be 'softmax' or 'sigmoid'")
-    r = Router(int(score == "sigmoid"), int(num_groups), int(topk_groups), int(group_top), int(bool(renormalize)),
-               float(scale))
-    sh = make_shape(T, 128, 128, E, E, top_k)
-    with _launch_on(logits.device, stream) as st:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-        w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-        _check(load_library().moe_route_scored(ctypes.byref(sh), ctypes.byref(r), _ptr(logits), _ptr(bias), _ptr(ids),
-                                               _ptr(w), st))
+    _expect(logits, torch.float32, index, (T, E), "logits")
+    if bias is not None:
+        _expect(bias, torch.float32, index, (E,), "bias")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    _check((_lib or load_library()).moe_route_scored(
+        _shape_ref(T, 128, 128, E, E, top_k), _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale),
+        logits.data_ptr(), None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(), _current_stream(index)))
     return ids, w
 
 
 def _rms_norm(x, residual, weight, eps, sum_out, bf16, int8, stream):
-    _need(x, torch.bfloat16, "x")
-    K, dev = x.shape[-1], x.device
-    rows = x.numel() // K if K else 0
-    _need_all(dev, (residual, torch.bfloat16, x.shape, "residual"), (weight, torch.bfloat16, (K,), "weight"),
-              (sum_out, torch.bfloat16, x.shape, "sum_out"))
-    with _launch_on(dev, stream) as st:
-        if residual is not None and sum_out is None:
+    index = _on_gpu(x, "x")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return _rms_norm(x, residual, weight, eps, sum_out, bf16, int8, None)
+    shape = x.shape
+    K = shape[-1]
+    _expect(x, torch.bfloat16, index, shape, "x")
+    _expect(weight, torch.bfloat16, index, (K,), "weight")
+    if residual is not None:
+        _expect(residual, torch.bfloat16, index, shape, "residual")
+        if sum_out is None:
             sum_out = torch.empty_like(x)
-        y = torch.empty_like(x) if bf16 else None
-        q = torch.empty(x.shape, dtype=torch.int8, device=dev) if int8 else None
-        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if int8 else None
-        _check(load_library().moe_rms_norm(rows, K, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(sum_out),
-                                           _ptr(y), _ptr(q), _ptr(s), st))
+        else:
+            _expect(sum_out, torch.bfloat16, index, shape, "sum_out")
+    y = torch.empty_like(x) if bf16 else None
+    q = torch.empty_like(x, dtype=torch.int8) if int8 else None
+    s = torch.empty(shape[:-1], dtype=torch.float32, device=x.device) if int8 else None
+    _check((_lib or load_library()).moe_rms_norm(
+        x.numel() // K if K else 0, K, x.data_ptr(), None if residual is None else residual.data_ptr(),
+        weight.data_ptr(), eps, None if residual is None else sum_out.data_ptr(), y.data_ptr() if bf16 else None,
+        q.data_ptr() if int8 else None, s.data_ptr() if int8 else None, _current_stream(index)))
     return y, q, s, sum_out
 
 
@@ -691,31 +710,42 @@ def add_rms_norm_int8(x: torch.Tensor, residual: torch.Tensor, weight: torch.Ten
 
 def int8_quantize(x: torch.Tensor, *, stream=None):
     """bf16 rows -> (codes int8, scales float32 per row): code * scale stands for the value."""
-    _need(x, torch.bfloat16, "x")
+    index = _on_gpu(x, "x")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return int8_quantize(x)
     K = x.shape[-1]
-    with _launch_on(x.device, stream) as st:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(load_library().moe_int8_quantize(x.numel() // K if K else 0, K, _ptr(x), _ptr(q), _ptr(s), st))
+    _expect(x, torch.bfloat16, index, x.shape, "x")
+    q = torch.empty_like(x, dtype=torch.int8)
+    s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _check((_lib or load_library()).moe_int8_quantize(x.numel() // K if K else 0, K, x.data_ptr(), q.data_ptr(),
+                                                      s.data_ptr(), _current_stream(index)))
     return q, s
 
 
 def dense_gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, *,
                     out_dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Dense W8A8 product: c [M, N] = (a [M, K] . wq [N, K]^T) * a_scale [M] * w_scale [N]."""
+    index = _on_gpu(a, "a")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return dense_gemm_w8a8(a, a_scale, wq, w_scale, out_dtype=out_dtype, out=out)
     if a.dim() != 2 or wq.dim() != 2:
         raise ValueError("a must be [M, K] and wq [N, K]")
     M, K = a.shape
-    N, dev = wq.shape[0], a.device
-    dt = _out_dtype(out, out_dtype)
-    _need_all(dev, (a, torch.int8, (M, K), "a"), (a_scale, torch.float32, (M,), "a_scale"),
-              (wq, torch.int8, (N, K), "wq"), (w_scale, torch.float32, (N,), "w_scale"),
-              (out, None if out is None else out.dtype, (M, N), "out"))
-    with _launch_on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        _check(load_library().moe_w8a8_dense_gemm(M, N, K, _ptr(a), _ptr(a_scale), _ptr(wq), _ptr(w_scale), _ptr(out),
-                                                  dt, st))
+    N = wq.shape[0]
+    _expect(a, torch.int8, index, (M, K), "a")
+    _expect(a_scale, torch.float32, index, (M,), "a_scale")
+    _expect(wq, torch.int8, index, (N, K), "wq")
+    _expect(w_scale, torch.float32, index, (N,), "w_scale")
+    if out is None:
+        dt = _out_dtype(out_dtype)
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    else:
+        dt = _out_dtype(out.dtype)
+        _expect(out, out.dtype, index, (M, N), "out")
+    _check((_lib or load_library()).moe_w8a8_dense_gemm(M, N, K, a.data_ptr(), a_scale.data_ptr(), wq.data_ptr(),
+                                                        w_scale.data_ptr(), out.data_ptr(), dt, _current_stream(index)))
     return out
 
 
@@ -725,26 +755,35 @@ def grouped_gemm_w8a8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets
                       stream=None) -> torch.Tensor:
     """Grouped W8A8 product over expert slabs; returns c [num_tokens*top_k, cols] (rows past the last routed one
     are not written). kind, offsets and a_row_index as in grouped_gemm_w4a16."""
+    index = _on_gpu(a, "a")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return grouped_gemm_w8a8(kind, a, a_scale, offsets, wq, w_scale, num_tokens=num_tokens, top_k=top_k,
+                                     a_row_index=a_row_index, out_dtype=out_dtype, num_experts=num_experts, out=out)
     if wq.dim() != 3:
         raise ValueError("wq must be [E, N, K]")
     E_loc, N, K = wq.shape
-    dev = a.device
     H, I = (N, K) if kind == W2 else (K, N // 2)
     cols = I if kind == W13_SWIGLU else N
     rows = num_tokens * top_k
     a_rows = rows if a_row_index is None else num_tokens
-    dt = _out_dtype(out, out_dtype)
-    _need_all(dev, (a, torch.int8, (a_rows, K), "a"), (a_scale, torch.float32, (a_rows,), "a_scale"),
-              (offsets, torch.int32, (E_loc + 1,), "offsets"), (wq, torch.int8, (E_loc, N, K), "wq"),
-              (w_scale, torch.float32, (E_loc, N), "w_scale"), (a_row_index, torch.int32, (rows,), "a_row_index"),
-              (out, None if out is None else out.dtype, (rows, cols), "out"))
-    sh = make_shape(num_tokens, H, I, num_experts or E_loc, E_loc, top_k, group_size=0)
-    with _launch_on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-        _check(load_library().moe_grouped_gemm_w8a8(ctypes.byref(sh), int(kind), _ptr(a), _ptr(a_scale),
-                                                    _ptr(a_row_index), _ptr(offsets), _ptr(wq), _ptr(w_scale),
-                                                    _ptr(out), dt, st))
+    _expect(a, torch.int8, index, (a_rows, K), "a")
+    _expect(a_scale, torch.float32, index, (a_rows,), "a_scale")
+    _expect(offsets, torch.int32, index, (E_loc + 1,), "offsets")
+    _expect(wq, torch.int8, index, (E_loc, N, K), "wq")
+    _expect(w_scale, torch.float32, index, (E_loc, N), "w_scale")
+    if a_row_index is not None:
+        _expect(a_row_index, torch.int32, index, (rows,), "a_row_index")
+    if out is None:
+        dt = _out_dtype(out_dtype)
+        out = torch.empty((rows, cols), dtype=out_dtype, device=a.device)
+    else:
+        dt = _out_dtype(out.dtype)
+        _expect(out, out.dtype, index, (rows, cols), "out")
+    _check((_lib or load_library()).moe_grouped_gemm_w8a8(
+        _shape_ref(num_tokens, H, I, num_experts or E_loc, E_loc, top_k, 0, 0), kind, a.data_ptr(), a_scale.data_ptr(),
+        None if a_row_index is None else a_row_index.data_ptr(), offsets.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+        out.data_ptr(), dt, _current_stream(index)))
     return out
 
 
@@ -755,30 +794,38 @@ def moe_w8a8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Ten
     """The W8A8 expert layer after routing: x int8 [T, H] with x_scale [T] (add_rms_norm_int8, int8_quantize),
     topk_ids / topk_w from route or route_scored, weights int8 [E_loc, 2I, H] / [E_loc, H, I] with a float32 scale per
     row. num_experts: the router's (default: all local). Returns out bf16 [T, H]."""
+    index = _on_gpu(x, "x")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return moe_w8a8_forward(x, x_scale, topk_ids, topk_w, w13_q, w13_s, w2_q, w2_s, out, num_experts=num_experts,
+                                    expert_begin=expert_begin, workspace=workspace)
     if x.dim() != 2 or topk_ids.dim() != 2 or w13_q.dim() != 3:
         raise ValueError("x must be [T, H], topk_ids [T, k] and w13_q [E, 2I, H]")
     T, H = x.shape
     k = topk_ids.shape[1]
     E_loc, N13, _ = w13_q.shape
-    I, dev = N13 // 2, x.device
-    _need_all(dev, (x, torch.int8, (T, H), "x"), (x_scale, torch.float32, (T,), "x_scale"),
-              (topk_ids, torch.int32, (T, k), "topk_ids"), (topk_w, torch.float32, (T, k), "topk_w"),
-              (w13_q, torch.int8, (E_loc, 2 * I, H), "w13_q"), (w13_s, torch.float32, (E_loc, 2 * I), "w13_s"),
-              (w2_q, torch.int8, (E_loc, H, I), "w2_q"), (w2_s, torch.float32, (E_loc, H), "w2_s"),
-              (out, torch.bfloat16, (T, H), "out"))
-    sh = make_shape(T, H, I, num_experts or expert_begin + E_loc, E_loc, k, expert_begin, group_size=0)
-    lib = load_library()
-    with _launch_on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        nbytes = int(lib.moe_w8a8_workspace_size(ctypes.byref(sh)))
-        if workspace is None:
-            # from the caching allocator at every call (about 1 us): it belongs to this stream, or to the graph that
-            # is being captured, so no two calls that can overlap share one
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        _check(lib.moe_w8a8_forward(ctypes.byref(sh), _ptr(x), _ptr(x_scale), _ptr(topk_ids), _ptr(topk_w), _ptr(w13_q),
-                                    _ptr(w13_s), _ptr(w2_q), _ptr(w2_s), _ptr(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), st))
+    I = N13 // 2
+    _expect(x, torch.int8, index, (T, H), "x")
+    _expect(x_scale, torch.float32, index, (T,), "x_scale")
+    _expect(topk_ids, torch.int32, index, (T, k), "topk_ids")
+    _expect(topk_w, torch.float32, index, (T, k), "topk_w")
+    _expect(w13_q, torch.int8, index, (E_loc, 2 * I, H), "w13_q")
+    _expect(w13_s, torch.float32, index, (E_loc, 2 * I), "w13_s")
+    _expect(w2_q, torch.int8, index, (E_loc, H, I), "w2_q")
+    _expect(w2_s, torch.float32, index, (E_loc, H), "w2_s")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _expect(out, torch.bfloat16, index, (T, H), "out")
+    lib = _lib or load_library()
+    sh = _shape_ref(T, H, I, num_experts or expert_begin + E_loc, E_loc, k, expert_begin, 0)
+    if workspace is None:
+        # from the caching allocator at every call: it belongs to this stream, or to the graph that is being captured,
+        # so no two calls that can overlap share one
+        workspace = torch.empty(max(lib.moe_w8a8_workspace_size(sh), 256), dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    _check(lib.moe_w8a8_forward(sh, x.data_ptr(), x_scale.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
+                                w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), out.data_ptr(),
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current_stream(index)))
     return out
