@@ -24,6 +24,7 @@ namespace {
 // A row whose largest magnitude is below 2^-100 counts as zero, so that neither
 // 1 / max overflows nor max / 127 meets a subnormal.
 constexpr float kZeroRow = 0x1p-100f;
+constexpr long long kFewRows = 1024;
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *s_red)
@@ -77,14 +78,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
     __shared__ float s_red[TPR / 64];
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const int lane = threadIdx.x % TPR;
-    long long rows = n.rows;
-    if (n.rows_dev) {
-        const long long d = n.rows_dev[0];
-        rows = d < rows ? d : rows;
-    }
     const long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
-    if (row >= rows)
+    if (row >= n.rows)
         return;                                        // whole workgroups where they meet at barriers
+    // Rows past the device's count: of few rows, read all the same (they are there) and left then, one round trip
+    // instead of two; of many, left at once.
+    if (n.rows_dev && n.rows >= kFewRows && row >= n.rows_dev[0])
+        return;
     const int V = n.K >> 3;
     const long long base = row * V;
     const u32x4 *x = reinterpret_cast<const u32x4 *>(n.x) + base;
@@ -104,6 +104,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
             const int v = lane + i * TPR, c = v < V ? v : V - 1;
             gv[i] = wt[c];
         }
+    if (n.rows_dev && n.rows < kFewRows && row >= n.rows_dev[0])
+        return;
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -209,8 +211,14 @@ hipError_t launch_rows(const NormLaunch &n, hipStream_t st)
 
 hipError_t launch_norm(const NormLaunch &n, hipStream_t st)
 {
+    // a wave per row while that takes at most two vectors a lane, or as long as there are rows enough to fill the
+    // GPU with waves: no barriers
     if (n.K <= 512)
         return launch_rows<64, 1>(n, st);
+    if (n.K <= 1024)
+        return launch_rows<64, 2>(n, st);
+    if (n.K <= 2048 && n.rows >= 2048)
+        return launch_rows<64, 4>(n, st);
     if (n.K <= 2048)
         return launch_rows<256, 1>(n, st);
     if (n.K <= 4096)

@@ -12,13 +12,15 @@
 //
 // A selection has to come out the same however it is computed, so the score
 // is the exact function's value rounded to binary32: the exponentials and
-// their sum are formed in binary64, whose error (about 2^-52) changes that
-// rounding for about one score in 2^27. Everything after it is a binary32
-// comparison or one addition.
+// their sum are formed in binary64 to about 2^-46, which changes that rounding
+// for about one score in 2^22, and a selection only where that score's
+// neighbour is the next binary32 number as well. Everything after it is a
+// binary32 comparison or one addition.
 //
-// One wave holds a token, lane q its experts q, q + 64, ...; k rounds take the
-// largest remaining key (the order-preserving integer image of c) by DPP and
-// retire it.
+// One wave holds a token, lane q its experts q PL .. q PL + PL - 1 (so groups
+// of experts are groups of neighbouring lanes, reduced by DPP); k rounds take
+// the largest remaining key (the order-preserving integer image of c) and
+// retire it. Bound by instructions: about 25 per exponential, 25 per round.
 #include "route_core.hpp"
 #include "w8a8.hpp"
 
@@ -43,48 +45,117 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-template <int PL>
+// exp(x) in binary64 for |x| <= 110 (x is clamped): x = n ln 2 + r with
+// |r| <= ln 2 / 2, the Taylor sum of exp(r) to r^11 / 11! (what is left out is
+// below 0.35^12 / 12! = 7e-15 of it), times 2^n.
+__device__ __forceinline__ double exp_clamped(double x)
+{
+    x = __builtin_fmin(__builtin_fmax(x, -110.0), 110.0);
+    const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
+    double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);       // ln 2 in two parts
+    r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);
+    double y = 1.0 / 39916800.0;
+    y = __builtin_fma(y, r, 1.0 / 3628800.0);
+    y = __builtin_fma(y, r, 1.0 / 362880.0);
+    y = __builtin_fma(y, r, 1.0 / 40320.0);
+    y = __builtin_fma(y, r, 1.0 / 5040.0);
+    y = __builtin_fma(y, r, 1.0 / 720.0);
+    y = __builtin_fma(y, r, 1.0 / 120.0);
+    y = __builtin_fma(y, r, 1.0 / 24.0);
+    y = __builtin_fma(y, r, 1.0 / 6.0);
+    y = __builtin_fma(y, r, 0.5);
+    y = __builtin_fma(y, r, 1.0);
+    y = __builtin_fma(y, r, 1.0);
+    return __builtin_ldexp(y, (int)n);
+}
+
+// 1 / d for 1 <= d < 2^200: the hardware's estimate and two Newton steps, each of which squares its error.
+__device__ __forceinline__ double reciprocal(double d)
+{
+    double y = __builtin_amdgcn_rcp(d);
+    y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+}
+
+// (a, b) and another lane's: the two largest of the four.
+__device__ __forceinline__ void merge_top2(uint32_t &a, uint32_t &b, uint32_t oa, uint32_t ob)
+{
+    const uint32_t lo = a < oa ? a : oa, hi = a < oa ? oa : a;
+    b = b > ob ? b : ob;
+    b = b > lo ? b : lo;
+    a = hi;
+}
+
+// GROUPS: 0 none; 1 a group is GL = 2^n whole lanes; 2 any.
+template <int PL, int GROUPS>
 __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
-    int T, int E, int k, moe_router r, const float *__restrict__ logits, const float *__restrict__ bias,
+    int T, int E, int k, moe_router r, const float *__restrict__ logits, const float *__restrict__ bias, bool vec,
     int32_t *__restrict__ ids, float *__restrict__ w)
 {
-    __shared__ uint32_t s_key[kScoredWaves][PL * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int t = blockIdx.x * kScoredWaves + wave;
     const bool there = t < T;
     const float *row = logits + (size_t)(there ? t : T - 1) * E;
+    const int e0 = lane * PL;
     float l[PL], b[PL];
+    if (vec) {                                         // a lane's experts are all there or none is
+        typedef float vecf __attribute__((ext_vector_type(PL < 4 ? PL : 4)));
+        constexpr int W = PL < 4 ? PL : 4;
+        const int at = e0 < E ? e0 : 0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = row[e < E ? e : E - 1];
-        b[i] = bias ? bias[e < E ? e : E - 1] : 0.0f;
+        for (int i = 0; i < PL; i += W) {
+            const vecf v = *reinterpret_cast<const vecf *>(row + at + i);
+            vecf c = {};
+            if (bias)
+                c = *reinterpret_cast<const vecf *>(bias + at + i);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if constexpr (W == 1) {
+                    l[i] = v[0];
+                    b[i] = c[0];
+                } else {
+                    l[i + j] = v[j];
+                    b[i + j] = c[j];
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int e = e0 + i < E ? e0 + i : E - 1;
+            l[i] = row[e];
+            b[i] = bias ? bias[e] : 0.0f;
+        }
     }
     float score[PL];
     if (r.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            score[i] = (float)(1.0 / (1.0 + exp(-(double)l[i])));
+            score[i] = l[i] == l[i] ? (float)reciprocal(1.0 + exp_clamped(-(double)l[i])) : l[i];
     } else {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-            const uint32_t o = lane + 64 * i < E && l[i] == l[i] ? ordered_bits(l[i]) : 0u;
+            const uint32_t o = e0 + i < E && l[i] == l[i] ? ordered_bits(l[i]) : 0u;
             m = o > m ? o : m;
         }
-        const double top = (double)from_ordered_bits(wave_max(m));
+        const float top = from_ordered_bits(wave_max(m));
         double p[PL], sum = 0.0;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-            p[i] = exp((double)l[i] - top);
-            sum += lane + 64 * i < E && p[i] == p[i] ? p[i] : 0.0;
+            // below -110 (e^-110 < 2^-150) the share rounds to 0; inf - inf (nothing is left, or an infinite logit) is NaN
+            const float d0 = l[i] - top;
+            const double d = (double)l[i] - (double)top;
+            p[i] = d0 < -110.0f ? 0.0 : (d0 == d0 ? exp_clamped(d) : (double)d0);
+            sum += e0 + i < E && p[i] == p[i] ? p[i] : 0.0;
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2)
             sum += __shfl_xor(sum, d);
+        const double inv = 1.0 / sum;
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            score[i] = (float)(p[i] / sum);
+            score[i] = (float)(p[i] * inv);
     }
     uint32_t key[PL];
 #pragma unroll
@@ -93,66 +164,89 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
         const bool masked = !(c == c) || l[i] == -__builtin_inff();
         score[i] = masked ? 0.0f : score[i];
         const uint32_t o = masked ? kMaskedKey : ordered_bits(c);
-        key[i] = lane + 64 * i < E ? o : kNoKey;
+        key[i] = e0 + i < E ? o : kNoKey;
     }
-    if (r.num_groups > 1) {
-        // lane g scores group g, then counts the groups ahead of it
+    if constexpr (GROUPS > 0) {
         const int G = r.num_groups, size = E / G;
+        uint32_t a = 0, b2 = 0;                        // the two largest keys of a group
+        int my_g, gl;                                  // the lane's group; lanes from one group's holder to the next's
+        if constexpr (GROUPS == 1) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i)
-            s_key[wave][lane + 64 * i] = key[i];
-        __syncthreads();
-        uint32_t a = 0, b2 = 0;                        // the two largest keys of the group
-        if (lane < G)
-            for (int i = 0; i < size; ++i) {
-                const uint32_t v = s_key[wave][lane * size + i];
-                b2 = v > a ? a : (v > b2 ? v : b2);
-                a = v > a ? v : a;
-            }
-        uint32_t gk = a;
-        if (r.group_top == 2)
-            gk = ordered_bits(from_ordered_bits(a) + from_ordered_bits(b2));
-        int ahead = 0;
-        for (int g = 0; g < G; ++g) {
-            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, g);
-            ahead += o > gk || (o == gk && g < lane);
+            for (int i = 0; i < PL; ++i)
+                merge_top2(a, b2, key[i], 0u);
+            gl = size / PL;
+            my_g = lane / gl;
+#define MOE_TOP2_STEP(n, ctrl)                                                                             \
+            if (gl > n)                                                                                    \
+                merge_top2(a, b2, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, ctrl, 0xF, 0xF, false), \
+                           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b2, ctrl, 0xF, 0xF, false));
+            MOE_TOP2_STEP(1, 0xB1)     // quad_perm [1,0,3,2]
+            MOE_TOP2_STEP(2, 0x4E)     // quad_perm [2,3,0,1]
+            MOE_TOP2_STEP(4, 0x141)    // row_half_mirror
+            MOE_TOP2_STEP(8, 0x140)    // row_mirror
+#undef MOE_TOP2_STEP
+            if (gl > 16)
+                merge_top2(a, b2, __shfl_xor(a, 16), __shfl_xor(b2, 16));
+            if (gl > 32)
+                merge_top2(a, b2, __shfl_xor(a, 32), __shfl_xor(b2, 32));
+        } else {
+            __shared__ uint32_t s_key[kScoredWaves][PL * 64];
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                s_key[wave][e0 + i] = key[i];
+            __syncthreads();
+            if (lane < G)                              // lane g holds group g
+                for (int i = 0; i < size; ++i)
+                    merge_top2(a, b2, s_key[wave][lane * size + i], 0u);
+            gl = 1;
+            my_g = lane;
         }
-        const uint64_t keep = __ballot(lane < G && ahead < r.topk_groups);
+        const uint32_t gk = r.group_top == 2 ? ordered_bits(from_ordered_bits(a) + from_ordered_bits(b2)) : a;
+        int ahead = 0;                                 // groups that come before this one
+        for (int g = 0; g < G; ++g) {
+            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, g * gl);
+            ahead += o > gk || (o == gk && g < my_g);
+        }
+        if constexpr (GROUPS == 1) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int e = lane + 64 * i;
-            if (e >= E || !(keep >> (e / size) & 1))
-                key[i] = kNoKey;
+            for (int i = 0; i < PL; ++i)
+                key[i] = ahead < r.topk_groups ? key[i] : kNoKey;
+        } else {
+            const uint64_t keep = __ballot(lane < G && ahead < r.topk_groups);
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const int e = e0 + i;
+                if (e >= E || !(keep >> (e / size) & 1))
+                    key[i] = kNoKey;
+            }
         }
     }
     int my_e = 0;
-    float my_s = 0.0f;
     for (int j = 0; j < k; ++j) {
-        uint32_t m = 0;
+        uint32_t bv = 0;
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            m = key[i] > m ? key[i] : m;
-        m = wave_max(m);
-        int e = 0;
+            bv = key[i] > bv ? key[i] : bv;
+        int at = 0;                                    // the lane's first expert that has it
 #pragma unroll
-        for (int i = PL - 1; i >= 0; --i) {
-            const uint64_t at = __ballot(key[i] == m);
-            if (at)
-                e = 64 * i + __builtin_ctzll(at);
-        }
-        float s = 0.0f;
+        for (int i = PL - 1; i >= 0; --i)
+            at = key[i] == bv ? i : at;
+        const uint32_t m = wave_max(bv);
+        const int owner = __builtin_ctzll(__ballot(bv == m));
+        const int e = __builtin_amdgcn_readlane(e0 + at, owner);
+        my_e = lane == j ? e : my_e;
+        if (lane == owner)
 #pragma unroll
-        for (int i = 0; i < PL; ++i)
-            if (lane + 64 * i == e) {
-                s = score[i];
-                key[i] = kNoKey;
-            }
-        s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), e & 63));
-        if (lane == j) {
-            my_e = e;
-            my_s = s;
-        }
+            for (int i = 0; i < PL; ++i)
+                key[i] = i == at ? kNoKey : key[i];
     }
+    float my_s = 0.0f;                                 // lane j < k: slot j's score, from the lane that has it
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const float v = __int_as_float(__builtin_amdgcn_ds_bpermute(my_e / PL * 4, __float_as_int(score[i])));
+        my_s = my_e % PL == i ? v : my_s;
+    }
+    my_s = lane < k ? my_s : 0.0f;
     float z = my_s;                                    // lanes >= k hold 0
 #define MOE_DPP_ADD(ctrl) z += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(z), ctrl, 0xF, 0xF, false));
     MOE_DPP_ADD(0xB1)      // quad_perm [1,0,3,2]
@@ -167,23 +261,39 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
     }
 }
 
+template <int PL>
+void launch_scored(int T, int E, int k, const moe_router &r, const float *logits, const float *bias, int32_t *ids,
+                   float *w, hipStream_t st)
+{
+    constexpr size_t W = PL < 4 ? PL : 4;              // values of a vector load
+    const bool vec = E % PL == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * W) == 0 &&
+                     reinterpret_cast<uintptr_t>(bias) % (4 * W) == 0;
+    const int size = E / r.num_groups, gl = size / PL;
+    const dim3 grid((T + kScoredWaves - 1) / kScoredWaves), block(kScoredWaves * 64);
+    if (r.num_groups == 1)
+        hipLaunchKernelGGL((route_scored_kernel<PL, 0>), grid, block, 0, st, T, E, k, r, logits, bias, vec, ids, w);
+    else if (size % PL == 0 && (gl & (gl - 1)) == 0)
+        hipLaunchKernelGGL((route_scored_kernel<PL, 1>), grid, block, 0, st, T, E, k, r, logits, bias, vec, ids, w);
+    else
+        hipLaunchKernelGGL((route_scored_kernel<PL, 2>), grid, block, 0, st, T, E, k, r, logits, bias, vec, ids, w);
+}
+
 }  // namespace
 
 hipError_t launch_route_scored(const moe_shape &sh, const moe_router &r, const float *logits, const float *bias,
                                int32_t *ids, float *w, hipStream_t st)
 {
     const int T = sh.num_tokens, E = sh.num_experts, k = sh.top_k;
-    const dim3 grid((T + kScoredWaves - 1) / kScoredWaves), block(kScoredWaves * 64);
     if (E <= 64)
-        hipLaunchKernelGGL((route_scored_kernel<1>), grid, block, 0, st, T, E, k, r, logits, bias, ids, w);
+        launch_scored<1>(T, E, k, r, logits, bias, ids, w, st);
     else if (E <= 128)
-        hipLaunchKernelGGL((route_scored_kernel<2>), grid, block, 0, st, T, E, k, r, logits, bias, ids, w);
+        launch_scored<2>(T, E, k, r, logits, bias, ids, w, st);
     else if (E <= 256)
-        hipLaunchKernelGGL((route_scored_kernel<4>), grid, block, 0, st, T, E, k, r, logits, bias, ids, w);
+        launch_scored<4>(T, E, k, r, logits, bias, ids, w, st);
     else if (E <= 512)
-        hipLaunchKernelGGL((route_scored_kernel<8>), grid, block, 0, st, T, E, k, r, logits, bias, ids, w);
+        launch_scored<8>(T, E, k, r, logits, bias, ids, w, st);
     else
-        hipLaunchKernelGGL((route_scored_kernel<kMaxExperts / 64>), grid, block, 0, st, T, E, k, r, logits, bias, ids, w);
+        launch_scored<kMaxExperts / 64>(T, E, k, r, logits, bias, ids, w, st);
     return hipGetLastError();
 }
 
