@@ -328,7 +328,8 @@ def test_refusals():
     assert ops.moe_w8a8_forward(xq[:0], xs[:0], ids[:0], tw[:0], w13, s13, w2, s2, out=out[:0]).shape == (0, 256)
 
 
-@pytest.mark.parametrize("T,E,k", [(3, 8, 4), (40, 8, 4), (300, 1024, 3), (500, 8, 4), (3000, 64, 16)])
+@pytest.mark.parametrize("T,E,k", [(1, 1024, 16), (3, 8, 4), (40, 8, 4), (64, 128, 16), (128, 1000, 8), (300, 1024, 3), (380, 8, 4),
+                                   (500, 8, 4), (3000, 64, 16)])
 def test_permute_with_an_expert_named_twice(T, E, k):
     """Both slots of such a token have the expert's one row for it, and every row below R holds a slot."""
     from w4a16_grouped_gemm_amd import ops

@@ -410,17 +410,17 @@ __device__ __forceinline__ void wait_for()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// The wait of an early step f < NS - 3, while copies that went out weights first
-// are still on their way: the tokens' of NS - 3 - f stages, and f whole stages.
-template <int NS, int LM, int L>
-__device__ __forceinline__ void early_wait(int f)
+// The wait of an early step s < NS - 3, while copies that went out weights first
+// are still on their way: the tokens' of NS - 3 - s stages, and s whole stages.
+template <int NS, int LM, int L, int F = 0>
+__device__ __forceinline__ void early_wait(int s)
 {
-    if (f == 0)
-        wait_for<(NS - 3) * LM>();
-    else if (f == 1)
-        wait_for<(NS > 4 ? NS - 4 : 0) * LM + L>();
-    else
-        wait_for<(NS > 5 ? NS - 5 : 0) * LM + 2 * L>();
+    if constexpr (F < NS - 3) {
+        if (s == F)
+            wait_for<(NS - 3 - F) * LM + F * L>();
+        else
+            early_wait<NS, LM, L, F + 1>(s);
+    }
 }
 
 template <int N>
@@ -628,10 +628,7 @@ __global__ __launch_bounds__(256, TN * TM > 8 ? 1 : 2) void w8_tile_kernel(W8Arg
     if (steps > NS - 1) {
         half_step(d0, d1, cur + f1, C0(), C0(), 0, 0);  // stage NS - 2 is already on its way
         for (;; ++s) {
-#pragma unroll
-            for (int f = 0; f < NS - 3; ++f)
-                if (s == f)
-                    early_wait<NS, LM, L>(f);
+            early_wait<NS, LM, L>(s);
             wait_barrier<(NS - 3) * L>();
             to = after(to);
             k += kStageK;

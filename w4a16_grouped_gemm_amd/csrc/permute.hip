@@ -388,6 +388,67 @@ __global__ __launch_bounds__(kPermThreads) void permute_kernel(
             perm[r] = -1;
 }
 
+// Few slots and experts (at most 1024 each): a thread per slot, and per expert.
+// The same tables as permute_kernel's, whose one-chunk path gives a thread a
+// token with its k slots one after another; 16 tokens of top-8 over 128 experts
+// 7.7 -> 2.6 us.
+__global__ __launch_bounds__(1024) void permute_small_kernel(int T, int k, int begin, int E, int words,
+                                                             const int32_t *__restrict__ ids,
+                                                             int32_t *__restrict__ counts,
+                                                             int32_t *__restrict__ offsets,
+                                                             int32_t *__restrict__ perm,
+                                                             int32_t *__restrict__ inv_perm)
+{
+    __shared__ int s_off[kMaxExperts];
+    __shared__ int s_wave_tot[1024 / 64];
+    extern __shared__ uint32_t s_dyn[];                  // [E][words]: bit t of expert e <=> token t routed to it
+    const int tid = threadIdx.x, S = T * k, waves = blockDim.x >> 6;
+    int e = tid < S ? ids[tid] - begin : -1;
+    for (int i = tid; i < E * words; i += blockDim.x)
+        s_dyn[i] = 0u;
+    e = e >= 0 && e < E ? e : -1;
+    const int t = tid / k;
+    __syncthreads();
+    if (e >= 0)
+        atomicOr(&s_dyn[e * words + (t >> 5)], 1u << (t & 31));
+    __syncthreads();
+    int cnt = 0;                                         // of expert tid
+    if (tid < E)
+        for (int w = 0; w < words; ++w)
+            cnt += __popc(s_dyn[tid * words + w]);
+    int wtot;
+    const int ex = wave_exclusive_scan(cnt, wtot);
+    if ((tid & 63) == 0)
+        s_wave_tot[tid >> 6] = wtot;
+    __syncthreads();
+    int base = 0, R = 0;
+    for (int w = 0; w < waves; ++w) {
+        const int v = s_wave_tot[w];
+        base += w < (tid >> 6) ? v : 0;
+        R += v;
+    }
+    if (tid < E) {
+        s_off[tid] = base + ex;
+        offsets[tid] = base + ex;
+        counts[tid] = cnt;
+    }
+    if (tid == 0)
+        offsets[E] = R;
+    __syncthreads();
+    if (tid < S) {
+        int row = -1;
+        if (e >= 0) {
+            row = s_off[e] + __popc(s_dyn[e * words + (t >> 5)] & ((1u << (t & 31)) - 1u));
+            for (int w = 0; w < t >> 5; ++w)
+                row += __popc(s_dyn[e * words + w]);
+            perm[row] = tid;
+        }
+        inv_perm[tid] = row;
+    }
+    for (int r = R + tid; r < S; r += blockDim.x)
+        perm[r] = -1;
+}
+
 // Parallel path, step 1: expert histogram of each workgroup's token range
 // (tpb tokens) -> part[b][e].
 __global__ __launch_bounds__(256) void permute_hist_kernel(int T, int k, int begin, int E, int tpb,
@@ -490,6 +551,13 @@ hipError_t launch_permute(const moe_shape &sh, const int32_t *ids, int32_t *coun
     const int E = sh.num_local_experts;
     const int T = sh.num_tokens;
     const int nb = parallel_ranges(sh);
+    const int words = (T + 31) / 32, slots = T * sh.top_k;
+    if (!nb && !num_shared && T > 0 && slots <= 1024 && E <= 1024 && (size_t)E * words * 4 <= (size_t)kMaskBytes) {
+        const int threads = ((slots > E ? slots : E) + 63) / 64 * 64;
+        hipLaunchKernelGGL(permute_small_kernel, dim3(1), dim3(threads), (size_t)E * words * 4, st, T, sh.top_k,
+                           sh.expert_begin, E, words, ids, counts, offsets, perm, inv_perm);
+        return hipGetLastError();
+    }
     const int tpb = nb ? (T + nb - 1) / nb : T;        // tokens per workgroup
     int chunk = chunk_tokens_for(E);
     while (chunk > 32 && chunk / 2 >= tpb)              // no wider than the token count needs

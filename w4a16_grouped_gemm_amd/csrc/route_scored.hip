@@ -12,15 +12,16 @@
 //
 // A selection has to come out the same however it is computed, so the score
 // is the exact function's value rounded to binary32: the exponentials and
-// their sum are formed in binary64 to about 2^-46, which changes that rounding
-// for about one score in 2^22, and a selection only where that score's
+// their sum are formed in binary64 to about 2^-42, which changes that rounding
+// for about one score in 2^17, and a selection only where that score's
 // neighbour is the next binary32 number as well. Everything after it is a
 // binary32 comparison or one addition.
 //
 // One wave holds a token, lane q its experts q PL .. q PL + PL - 1 (so groups
 // of experts are groups of neighbouring lanes, reduced by DPP); k rounds take
 // the largest remaining key (the order-preserving integer image of c) and
-// retire it. Bound by instructions: about 25 per exponential, 25 per round.
+// retire it. Bound by instructions (about 600 per token, the vector units 85%
+// busy): 8192 tokens of 256 experts in 8 groups, top 8: 10.4 us.
 #include "route_core.hpp"
 #include "w8a8.hpp"
 
@@ -45,17 +46,15 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// exp(x) in binary64 for |x| <= 110 (x is clamped): x = n ln 2 + r with
-// |r| <= ln 2 / 2, the Taylor sum of exp(r) to r^11 / 11! (what is left out is
-// below 0.35^12 / 12! = 7e-15 of it), times 2^n.
-__device__ __forceinline__ double exp_clamped(double x)
+// exp(x) in binary64 for |x| <= 110: x = n ln 2 + r with |r| <= ln 2 / 2, the
+// Taylor sum of exp(r) to r^10 / 10! (what is left out is below 0.35^11 / 11!
+// = 2e-13 of it), times 2^n.
+__device__ __forceinline__ double exp_near(double x)
 {
-    x = __builtin_fmin(__builtin_fmax(x, -110.0), 110.0);
     const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
     double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);       // ln 2 in two parts
     r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);
-    double y = 1.0 / 39916800.0;
-    y = __builtin_fma(y, r, 1.0 / 3628800.0);
+    double y = 1.0 / 3628800.0;
     y = __builtin_fma(y, r, 1.0 / 362880.0);
     y = __builtin_fma(y, r, 1.0 / 40320.0);
     y = __builtin_fma(y, r, 1.0 / 5040.0);
@@ -69,11 +68,10 @@ __device__ __forceinline__ double exp_clamped(double x)
     return __builtin_ldexp(y, (int)n);
 }
 
-// 1 / d for 1 <= d < 2^200: the hardware's estimate and two Newton steps, each of which squares its error.
+// 1 / d for 1 <= d < 2^200: the hardware's estimate (2^-23 or better) and a Newton step, which squares its error.
 __device__ __forceinline__ double reciprocal(double d)
 {
-    double y = __builtin_amdgcn_rcp(d);
-    y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+    const double y = __builtin_amdgcn_rcp(d);
     return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
@@ -131,7 +129,8 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
     if (r.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            score[i] = l[i] == l[i] ? (float)reciprocal(1.0 + exp_clamped(-(double)l[i])) : l[i];
+            // past 110 either way it is 0 or 1 in binary32 (a NaN is masked below)
+            score[i] = (float)reciprocal(1.0 + exp_near(-(double)__builtin_amdgcn_fmed3f(l[i], -110.0f, 110.0f)));
     } else {
         uint32_t m = 0;
 #pragma unroll
@@ -145,8 +144,8 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
         for (int i = 0; i < PL; ++i) {
             // below -110 (e^-110 < 2^-150) the share rounds to 0; inf - inf (nothing is left, or an infinite logit) is NaN
             const float d0 = l[i] - top;
-            const double d = (double)l[i] - (double)top;
-            p[i] = d0 < -110.0f ? 0.0 : (d0 == d0 ? exp_clamped(d) : (double)d0);
+            p[i] = exp_near(__builtin_fmax((double)l[i] - (double)top, -110.0));
+            p[i] = d0 < -110.0f ? 0.0 : (d0 == d0 ? p[i] : (double)d0);
             sum += e0 + i < E && p[i] == p[i] ? p[i] : 0.0;
         }
 #pragma unroll
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         const float c = score[i] + b[i];
-        const bool masked = !(c == c) || l[i] == -__builtin_inff();
+        const bool masked = !(c == c) || !(l[i] > -__builtin_inff());          // NaN too
         score[i] = masked ? 0.0f : score[i];
         const uint32_t o = masked ? kMaskedKey : ordered_bits(c);
         key[i] = e0 + i < E ? o : kNoKey;
@@ -202,10 +201,10 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
             my_g = lane;
         }
         const uint32_t gk = r.group_top == 2 ? ordered_bits(from_ordered_bits(a) + from_ordered_bits(b2)) : a;
-        int ahead = 0;                                 // groups that come before this one
-        for (int g = 0; g < G; ++g) {
+        int ahead = 0;                                 // groups that come before this one: earlier ones with as large a
+        for (int g = 0; g < G; ++g) {                  // key, later ones with a larger one (no key is 2^32 - 1)
             const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, g * gl);
-            ahead += o > gk || (o == gk && g < my_g);
+            ahead += o >= gk + (g < my_g ? 0u : 1u);
         }
         if constexpr (GROUPS == 1) {
 #pragma unroll
@@ -222,23 +221,59 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
         }
     }
     int my_e = 0;
-    for (int j = 0; j < k; ++j) {
-        uint32_t bv = 0;
+    if constexpr (PL <= 4) {
+        // A lane's keys in descending order (neighbours change places only where the second is larger, so equal ones
+        // stay in index order), which expert each one was in the bytes of `which`: its largest is then always the first.
+        int at[PL];
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            bv = key[i] > bv ? key[i] : bv;
-        int at = 0;                                    // the lane's first expert that has it
+            at[i] = i;
 #pragma unroll
-        for (int i = PL - 1; i >= 0; --i)
-            at = key[i] == bv ? i : at;
-        const uint32_t m = wave_max(bv);
-        const int owner = __builtin_ctzll(__ballot(bv == m));
-        const int e = __builtin_amdgcn_readlane(e0 + at, owner);
-        my_e = lane == j ? e : my_e;
-        if (lane == owner)
+        for (int round = 0; round < PL; ++round)
+#pragma unroll
+            for (int i = round & 1; i + 1 < PL; i += 2) {
+                const uint32_t a = key[i], c = key[i + 1];
+                const int ia = at[i], ic = at[i + 1];
+                const bool swap = c > a;
+                key[i] = swap ? c : a;
+                key[i + 1] = swap ? a : c;
+                at[i] = swap ? ic : ia;
+                at[i + 1] = swap ? ia : ic;
+            }
+        uint32_t which = 0;
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            which |= (uint32_t)at[i] << (8 * i);
+        for (int j = 0; j < k; ++j) {
+            const uint32_t m = wave_max(key[0]);
+            const int owner = __builtin_ctzll(__ballot(key[0] == m));
+            const int e = __builtin_amdgcn_readlane(e0 + (int)(which & 255u), owner);
+            my_e = lane == j ? e : my_e;
+            const bool mine = lane == owner;
 #pragma unroll
             for (int i = 0; i < PL; ++i)
-                key[i] = i == at ? kNoKey : key[i];
+                key[i] = mine ? (i + 1 < PL ? key[i + 1 < PL ? i + 1 : i] : kNoKey) : key[i];
+            which = mine ? which >> 8 : which;
+        }
+    } else {
+        for (int j = 0; j < k; ++j) {
+            uint32_t bv = 0;
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                bv = key[i] > bv ? key[i] : bv;
+            int at = 0;                                // the lane's first expert that has it
+#pragma unroll
+            for (int i = PL - 1; i >= 0; --i)
+                at = key[i] == bv ? i : at;
+            const uint32_t m = wave_max(bv);
+            const int owner = __builtin_ctzll(__ballot(bv == m));
+            const int e = __builtin_amdgcn_readlane(e0 + at, owner);
+            my_e = lane == j ? e : my_e;
+            if (lane == owner)
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    key[i] = i == at ? kNoKey : key[i];
+        }
     }
     float my_s = 0.0f;                                 // lane j < k: slot j's score, from the lane that has it
 #pragma unroll

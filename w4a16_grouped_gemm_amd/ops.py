@@ -644,8 +644,8 @@ def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None 
     _expect(logits, torch.float32, index, (T, E), "logits")
     if bias is not None:
         _expect(bias, torch.float32, index, (E,), "bias")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
+    w = torch.empty_like(ids, dtype=torch.float32)
     _check((_lib or load_library()).moe_route_scored(
         _shape_ref(T, 128, 128, E, E, top_k), _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale),
         logits.data_ptr(), None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(), _current_stream(index)))
