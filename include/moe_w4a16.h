@@ -409,7 +409,8 @@ moe_status moe_w4a4_forward(const moe_shape *shape, const uint16_t *x, const flo
  * so that whatever is computed from it is NaN.
  *   x, residual, sum, y  bf16 [rows][K]; weight bf16 [K]
  *   q int8 [rows][K], q_scale f32 [rows]
- * At least one of y and q. eps >= 0. sum and y may be x or residual themselves
+ * At least one of y and q. eps >= 0. Fewer than 2^25 rows for K <= 1024, 2^23
+ * for K <= 16384, 2^21 beyond (MOE_ERR_UNSUPPORTED). sum and y may be x or residual themselves
  * (in place); any other overlap with an output gives MOE_ERR_UNSUPPORTED.
  */
 moe_status moe_rms_norm(int64_t rows, int32_t K, const uint16_t *x, const uint16_t *residual, const uint16_t *weight,

@@ -25,6 +25,12 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return a && b && x < y + nb && y < x + na;
 }
 
+// Rows of one norm or quantizer launch: fewer than 2^32 threads (a wave, 256 or 1024 threads per row).
+bool norm_rows_fit(int64_t rows, int32_t K)
+{
+    return rows < (1LL << (K <= 1024 ? 25 : K <= 16384 ? 23 : 21)) && rows * (int64_t)K * 2 < (1LL << 40);
+}
+
 // The layer's limits with one scale per row (group_size 0) and plain codes.
 moe_status check_shape_w8(const moe_shape *sh, moe_shape *s)
 {
@@ -121,7 +127,7 @@ moe_status moe_rms_norm(int64_t rows, int32_t K, const uint16_t *x, const uint16
 {
     if (rows < 0 || K < 8 || K % 8 != 0 || K > kMaxNormDim || !(eps >= 0.0f))
         return MOE_ERR_SHAPE;
-    if (rows >= (1LL << 31) || rows * (int64_t)K * 2 >= (1LL << 40))
+    if (!norm_rows_fit(rows, K))
         return MOE_ERR_UNSUPPORTED;
     if (rows == 0)
         return MOE_OK;
@@ -152,7 +158,7 @@ moe_status moe_int8_quantize(int64_t rows, int32_t K, const uint16_t *x, int8_t 
 {
     if (rows < 0 || K < 8 || K % 8 != 0 || K > kMaxNormDim)
         return MOE_ERR_SHAPE;
-    if (rows >= (1LL << 31) || rows * (int64_t)K * 2 >= (1LL << 40))
+    if (!norm_rows_fit(rows, K))
         return MOE_ERR_UNSUPPORTED;
     if (rows == 0)
         return MOE_OK;

@@ -385,6 +385,15 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // A weight row's place decides which output a result register is: tile t's row
 // r holds output ((r >> 2) & 1) 16 TG + 16 t + 4 (r >> 3) + (r & 3) of the
 // wave's columns, which makes a lane's sixteen results of a tile consecutive.
+//
+// 256 x 256 is the largest tile that four waves' accumulators (256 of a lane's
+// 512 registers) hold, and LDS traffic asks for it: per 64 bytes of K a CU moves
+// 64 KiB out of LDS and 32 KiB into it, 768 cycles at 128 B per cycle, beside
+// 1024 cycles of MFMA. Dense 8192 x 14336 x 4096: 433 us, 2.22 POP/s, the matrix
+// units 63% busy at 1.6 GHz (the clock that this load is given; 4.6 POP/s at
+// 2.4 GHz for MFMAs alone). The small tiles are bound by the weight stream:
+// 128 experts of 2048 -> 2 x 768, 64 tokens, 71 us, 5.6 TB/s with every byte
+// fetched once.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 64;
 
@@ -710,11 +719,19 @@ __global__ __launch_bounds__(256, TN * TM > 8 ? 1 : 2) void w8_tile_kernel(W8Arg
     }
 }
 
+// A kernel's LDS limit is raised once on each device that launches it.
 template <int KIND, bool F32, int TN, int TM, int NWN, int NWM, int NS>
 void allow_lds(int bytes)
 {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM, NS>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr int kMaxDevices = 64;
+    static std::once_flag once[kMaxDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
+        return;
+    std::call_once(once[dev], [bytes] {
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM, NS>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
 }
 
 template <int KIND, bool F32, int TN, int TM, int NWN, int NWM, int NS>
@@ -722,30 +739,33 @@ hipError_t launch_tile(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 {
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
     constexpr int BN = 32 * TN * NWN, BM = 32 * TM * NWM, BC = SW ? BN / 2 : BN;
-    constexpr int lds = (BN + BM) * kStageK * NS;      // 256 x 256: all of a CU's; 128 x 128: two workgroups to a CU
+    constexpr int lds = (BN + BM) * kStageK * NS;       // 256 x 256: all of a CU's; the others: two workgroups to a CU
     const int cols = SW ? g.N / 2 : g.N;
     const int tn = (cols + BC - 1) / BC;
     const long long tm = chunks_at_most(g, BM);
-    static std::once_flag once;
-    std::call_once(once, allow_lds<KIND, F32, TN, TM, NWN, NWM, NS>, lds);
+    allow_lds<KIND, F32, TN, TM, NWN, NWM, NS>(lds);
     hipLaunchKernelGGL((w8_tile_kernel<KIND, F32, TN, TM, NWN, NWM, NS>), dim3((unsigned)(tm * tn)), dim3(256), lds, st, p,
                        tn);
     return hipGetLastError();
 }
 
-// Which kernel, from the expected rows per expert with rows, R', and the tiles
-// (items) that each would have; us on MI355X, weights read from HBM:
-//   few items, R' <= 32: the streaming kernel, K split over the waves, since 128 x 64 tiles
-//     leave CUs idle: dense 16 x 14336 x 4096 16.5 against 23.0, 1 x 4096 x 4096 8.2 against 13.0,
-//     32 x 4096 x 4096 11.8 against 14.0
-//   R' up to 40 (spread over the experts; 64 where it is exact): 64-row tiles; 256 columns of
-//     weights once that fills two workgroups per CU (128 experts 2048 -> 2 x 768: 64 tokens 71.3
-//     against 72.7 with 128, 256 tokens 74.5 against 79.8, 256 x 128 tiles 80.9)
-//   above: 128-row tiles, 256 columns where that fills the GPU (32 experts 7168 -> 2 x 2048, 64 rows
-//     each: 190 against 204 with 128 and 266 with 64 rows), else 128 (dense 256 x 14336 x 4096 30
-//     against 42), and 64 rows again where even those leave CUs idle (333 x 2064 x 768: 5.9
-//     against 7.1)
-//   256 x 256 where it gives nearly every CU a tile (4096 x 4096 x 7168: 118 against 152)
+// Which kernel, from the expected rows R' of an expert that has any and the
+// tiles (items) that each kernel would have; us on MI355X, operands rotating
+// through more than the 256 MB memory-side cache:
+//   R' <= 32 and few items: the streaming kernel, K split over a workgroup's waves, since
+//     128 x 64 tiles leave CUs idle: dense 16 x 14336 x 4096 16.4 against 23.0 (M x N x K), 1 x 4096 x
+//     4096 5.9 against 13.0, 32 x 4096 x 4096 11.8 against 14.0. A wave has as many tiles as leave
+//     most CUs a workgroup: 1 x 4096 x 4096 with one 5.9, two 8.2, four 13.1; 16 x 14336 x 4096
+//     19.6, 16.7, 16.4
+//   R' <= 40 (rows spread over experts; 64 where the count is exact): tiles of 64 rows, of 256
+//     weight rows where that gives 1.5 workgroups per CU, else 128 (128 experts, 2048 -> 2 x 768:
+//     64 tokens 70.9 against 72.7, 256 tokens 73.9 against 79.8; 256 x 128 tiles 78.4 and 80.8)
+//   above: 128 rows, with 256 weight rows where that gives 1.5 workgroups per CU (32 experts,
+//     7168 -> 2 x 2048, 64 rows each: 188 against 204 with 128; tiles of 64 rows 266), else 128 (dense
+//     256 x 14336 x 4096 29 against 53), and 64 rows where those leave CUs idle (333 x 2064 x
+//     768: 5.9 against 7.1)
+//   256 x 256 where it gives nearly every CU a tile (dense 4096 x 4096 x 7168 112 against 132 with
+//     256 x 128 and 159 with 128 x 128)
 template <int KIND, bool F32>
 hipError_t launch_kind(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 {
@@ -758,9 +778,6 @@ hipError_t launch_kind(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
         const int BC = SW ? BN / 2 : BN;
         return reached * ceil(per / BM) * ((cols + BC - 1) / BC);
     };
-#ifdef CFG
-    return CFG(g, p, st);
-#endif
     if (per <= 32.0 && items(128, 64) < 256.0) {
         // a wave's tiles: as many as still give most CUs a workgroup
         const bool few4 = items(64, 64) < 192.0, few2 = items(32, 64) < 192.0;
