@@ -186,8 +186,10 @@ __device__ __forceinline__ bool find_tile(const W8Args &p, int CS, int tn, int b
 // bytes of K ahead, and multiplies them with NSUB subtiles of 16 tokens, whose
 // rows it fetches the same way (they stay in the caches). WK waves of a
 // workgroup share a set of rows, each with its part of K, and add their sums
-// (integers, so in any order) through LDS; else no LDS and no barrier. The
-// weights are read once, non-temporally.
+// (integers, so in any order) through LDS; else no LDS and no barrier. Default
+// cache policy: a load takes 64 bytes of each row, half a line, and non-temporal
+// ones lose the other half before the next load asks for it (1 x 4096 x 4096
+// 6.1 us against 5.3, one token through 128 experts' gate/up 9.0 against 8.1).
 // ---------------------------------------------------------------------------
 template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING>
 __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
@@ -246,7 +248,7 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
         for (int t = 0; t < TPW; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w[j][t][h] = bload16_codes<true>(rw, wo[t] + 64 * h, k);
+                w[j][t][h] = bload16(rw, wo[t] + 64 * h, k);
     };
     auto load_x = [&](int j, uint32_t k) {
 #pragma unroll
@@ -753,10 +755,10 @@ hipError_t launch_tile(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // tiles (items) that each kernel would have; us on MI355X, operands rotating
 // through more than the 256 MB memory-side cache:
 //   R' <= 32 and few items: the streaming kernel, K split over a workgroup's waves, since
-//     128 x 64 tiles leave CUs idle: dense 16 x 14336 x 4096 16.4 against 23.0 (M x N x K), 1 x 4096 x
-//     4096 5.9 against 13.0, 32 x 4096 x 4096 11.8 against 14.0. A wave has as many tiles as leave
+//     128 x 64 tiles leave CUs idle: dense 16 x 14336 x 4096 16.3 against 23.0 (M x N x K), 1 x 4096 x
+//     4096 5.3 against 13.0, 30 x 4096 x 4096 9.9 against 14.0. A wave has as many tiles as leave
 //     most CUs a workgroup: 1 x 4096 x 4096 with one 5.9, two 8.2, four 13.1; 16 x 14336 x 4096
-//     19.6, 16.7, 16.4
+//     19.6, 16.7, 16.4 (before the default policy)
 //   R' <= 40 (rows spread over experts; 64 where the count is exact): tiles of 64 rows, of 256
 //     weight rows where that gives 1.5 workgroups per CU, else 128 (128 experts, 2048 -> 2 x 768:
 //     64 tokens 70.9 against 72.7, 256 tokens 73.9 against 79.8; 256 x 128 tiles 78.4 and 80.8)
