@@ -152,3 +152,12 @@ def test_no_rows():
     q, s, h = ops.add_rms_norm_int8(e, e.clone(), w)
     assert q.shape == (0, 256) and s.shape == (0,) and h.shape == (0, 256)
     assert ops.int8_quantize(e)[1].shape == (0,)
+
+
+def test_refuses_a_tensor_without_dimensions():
+    from w4a16_grouped_gemm_amd import ops
+    x = torch.zeros((), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(8, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: ops.rms_norm(x, w), lambda: ops.add_rms_norm_int8(x, x, w), lambda: ops.int8_quantize(x)):
+        with pytest.raises(ValueError):
+            call()

@@ -99,6 +99,46 @@ def test_ties_masks_and_nan(G, kept, top, score):
     check(l, b, 6, score, G, kept, top, False, 0.5)
 
 
+MANY = [  # E, k, G, kept, top
+    (256, 8, 8, 4, 2), (256, 16, 1, 1, 1), (250, 7, 1, 1, 1), (129, 5, 1, 1, 1), (128, 8, 4, 2, 1), (120, 6, 3, 2, 2),
+    (96, 16, 4, 2, 2), (64, 6, 8, 3, 2), (60, 4, 5, 3, 2), (33, 3, 1, 1, 1), (8, 8, 1, 1, 1), (1, 1, 1, 1, 1), (160, 6, 8, 3, 1)]
+
+
+@pytest.mark.parametrize("E,k,G,kept,top", MANY)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_many_tokens(E, k, G, kept, top, score, offset):
+    """Each of 23 rows (ordinary, tied, masked, NaN) many times over, at every place of a workgroup; odd addresses."""
+    say(f"route_scored many E={E} k={k} G={G} kept={kept} top={top} {score} offset={offset}")
+    from w4a16_grouped_gemm_amd import ops
+    rng = np.random.default_rng(E * 7 + k)
+    l = (rng.standard_normal((23, E)) * 1.5).astype(np.float32)
+    l[1] = 0.0
+    l[2] = -np.inf
+    l[3] = rng.integers(-2, 3, E)
+    l[4, ::2] = -np.inf
+    l[5, E // 2:] = -np.inf
+    l[6, E // 3] = np.nan
+    l[7] = 40.0
+    l[8] = -200.0
+    l[8, E // 2] = 0.0
+    l[9] = rng.integers(0, 2, E)
+    b = (rng.standard_normal(E) * (0.1 if score == "sigmoid" else 0.1 / E)).astype(np.float32)
+    T = 4096 + 23
+    rows = torch.arange(T) * 5 % 23
+    for bias in (b, None):
+        x = torch.empty(T * E + offset, device="cuda")[offset:].view(T, E)
+        x.copy_(torch.from_numpy(l)[rows])
+        y = None
+        if bias is not None:
+            y = torch.empty(E + offset, device="cuda")[offset:]
+            y.copy_(torch.from_numpy(bias))
+        ids, w = ops.route_scored(x, k, bias=y, score=score, num_groups=G, topk_groups=kept, group_top=top, scale=2.5)
+        rid, rw = reference(l, bias, k, score, G, kept, top, True, 2.5)
+        assert np.array_equal(ids.cpu().numpy(), rid[rows])
+        assert (np.abs(w.cpu().numpy() - rw[rows]) <= 8 * 2.0 ** -24 * np.abs(rw[rows]) + 2.0 ** -148).all()
+
+
 def test_infinite_logit_and_no_tokens():
     from w4a16_grouped_gemm_amd import ops
     l = np.zeros((2, 16), np.float32)
@@ -132,3 +172,10 @@ def test_refusals():
         ops.route_scored(l, 17)
     with pytest.raises(ValueError):
         ops.route_scored(l.t(), 2)
+
+
+@pytest.mark.parametrize("k", [0, -1])
+def test_refuses_no_slots(k):
+    from w4a16_grouped_gemm_amd import ops
+    with pytest.raises(ValueError):
+        ops.route_scored(torch.zeros(4, 32, device="cuda"), k)

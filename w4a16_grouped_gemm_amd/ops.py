@@ -638,8 +638,8 @@ def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None 
         with there:
             return route_scored(logits, top_k, bias=bias, score=score, num_groups=num_groups, topk_groups=topk_groups,
                                 group_top=group_top, renormalize=renormalize, scale=scale)
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
+    if logits.dim() != 2 or top_k < 1:
+        raise ValueError("logits must be [T, E] and top_k at least 1")
     T, E = logits.shape
     _expect(logits, torch.float32, index, (T, E), "logits")
     if bias is not None:
@@ -658,7 +658,7 @@ def _rms_norm(x, residual, weight, eps, sum_out, bf16, int8, stream):
         with there:
             return _rms_norm(x, residual, weight, eps, sum_out, bf16, int8, None)
     shape = x.shape
-    K = shape[-1]
+    K = shape[-1] if shape else 0
     _expect(x, torch.bfloat16, index, shape, "x")
     _expect(weight, torch.bfloat16, index, (K,), "weight")
     if residual is not None:
@@ -714,7 +714,7 @@ def int8_quantize(x: torch.Tensor, *, stream=None):
     if (there := _elsewhere(index, stream)) is not None:
         with there:
             return int8_quantize(x)
-    K = x.shape[-1]
+    K = x.shape[-1] if x.shape else 0
     _expect(x, torch.bfloat16, index, x.shape, "x")
     q = torch.empty_like(x, dtype=torch.int8)
     s = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
