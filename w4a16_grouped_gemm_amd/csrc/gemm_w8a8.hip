@@ -24,14 +24,6 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 w, u32x4 x, i32x4 c)
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), c, 0, 0, 0);
 }
 
-// fp32 pair -> bf16 pair, round to nearest even
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
-{
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
-}
-
 struct W8Args {
     const int8_t *a;
     uint32_t a_bytes;

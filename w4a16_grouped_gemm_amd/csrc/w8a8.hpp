@@ -9,6 +9,14 @@ namespace moe {
 constexpr int kMaxNormDim = 65536;       // row length of the norm and the int8 quantizer
 constexpr int kMaxRouteGroups = 64;      // one lane of a wave per group
 
+// fp32 pair -> bf16 pair, round to nearest even
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
+}
+
 hipError_t launch_route_scored(const moe_shape &sh, const moe_router &r, const float *logits, const float *bias,
                                int32_t *ids, float *w, hipStream_t st);
 
