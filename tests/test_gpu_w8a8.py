@@ -144,6 +144,21 @@ def test_grouped(T, E, begin, L, k, H, I, mode):
                        run(ops.W13_SWIGLU, x, xs, w13, s13, I, B, perm))
 
 
+@pytest.mark.parametrize("H,I", [(128, 384), (640, 128), (640, 256), (640, 384), (768, 512), (896, 640), (1024, 768), (1920, 896),
+                                 (2048, 1024), (2176, 1920), (2304, 2048), (2432, 2176), (2560, 2304), (4096, 2432)])
+def test_grouped_few_rows(H, I):
+    """A few rows of each of 64 experts: every length of what is left of K after whole rounds of the weight stream."""
+    test_grouped(64, 64, 0, 64, 2, H, I, "uniform")
+    test_grouped(70, 64, 0, 64, 3, H, I, "zipf")
+
+
+@pytest.mark.parametrize("M", [1, 9, 16])
+@pytest.mark.parametrize("N", [14336, 12304])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 1152, 2432])
+def test_dense_few_rows(M, N, K):
+    test_dense(M, N, K)
+
+
 def layer_inputs(T, E, begin, L, k, H, I, mode, seed):
     g = gen(seed)
     ids = routing(T, E, k, g, mode)

@@ -4,9 +4,10 @@
 //   acc[r][n] = sum_k a[r][k] w[n][k]          exact, binary integer
 //   c[r][n]   = float(acc) * as[r] * ws[n]     (binary32)
 //
-// MFMA: v_mfma_i32_16x16x64_i8, the weight rows as operand A and the tokens as
-// operand B, so that a result lane holds four consecutive outputs of one token.
-// Both operands take the same permutation of K, which leaves the sums as they are.
+// MFMA: v_mfma_i32_16x16x64_i8 (streaming kernel) and 32x32x32 (tile kernel), the
+// weight rows as operand A and the tokens as operand B, so that a result lane
+// holds four (four times four) consecutive outputs of one token. Both operands
+// take the same permutation of K, which leaves the sums as they are.
 #include <cmath>
 #include <mutex>
 
@@ -182,6 +183,8 @@ __device__ __forceinline__ bool find_tile(const W8Args &p, int CS, int tn, int b
 // cache policy: a load takes 64 bytes of each row, half a line, and non-temporal
 // ones lose the other half before the next load asks for it (1 x 4096 x 4096
 // 6.1 us against 5.3, one token through 128 experts' gate/up 9.0 against 8.1).
+// Bound by the weight stream: 128 experts of 2048 -> 2 x 768, 64 tokens, 69 us,
+// 5.8 TB/s. Groups left over after whole rounds are fetched together as well.
 // ---------------------------------------------------------------------------
 template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING>
 __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
@@ -258,9 +261,9 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
                 for (int t = 0; t < TPW; ++t)
                     acc[s][t] = mfma_i8(w[j][t][h], x[j][s][h], acc[s][t]);
     };
-    // groups [g, end) of this wave, in rounds of RING: while a round is multiplied the next one is on its way
-    const int G = p.K / 128, end = (wk + 1) * G / WK;
-    int g = wk * G / WK;
+    // n groups from g on are this wave's, in rounds of RING: while a round is multiplied the next one is on its way
+    const int G = p.K / 128;
+    int g = wk * G / WK, n = (wk + 1) * G / WK - g;
     float as[NSUB];
     auto find_rows = [&]() {
 #pragma unroll
@@ -270,35 +273,49 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
             as[s] = p.as[ar];
         }
     };
-    if (end - g >= RING) {
-        // the first round's weights set out before the tokens' rows are known
+    auto at = [&](int j) { return (uint32_t)(g + j) * 128; };
+    // the first round's weights set out before the tokens' rows are known
+    if (n >= RING) {
 #pragma unroll
         for (int j = 0; j < RING; ++j)
-            load_w(j, (uint32_t)(g + j) * 128);
+            load_w(j, at(j));
         __builtin_amdgcn_sched_barrier(0);
         find_rows();
 #pragma unroll
         for (int j = 0; j < RING; ++j)
-            load_x(j, (uint32_t)(g + j) * 128);
-        for (; end - g >= 2 * RING; g += RING)
+            load_x(j, at(j));
+        for (; n >= 2 * RING; n -= RING, g += RING)
 #pragma unroll
             for (int j = 0; j < RING; ++j) {
                 multiply(j);
-                load_w(j, (uint32_t)(g + RING + j) * 128);
-                load_x(j, (uint32_t)(g + RING + j) * 128);
+                load_w(j, at(RING + j));
+                load_x(j, at(RING + j));
             }
+        n -= RING;
 #pragma unroll
-        for (int j = 0; j < RING; ++j)
+        for (int j = 0; j < RING; ++j) {
             multiply(j);
-        g += RING;
+            if (j < n) {
+                load_w(j, at(RING + j));
+                load_x(j, at(RING + j));
+            }
+        }
     } else {
+#pragma unroll
+        for (int j = 0; j < RING - 1; ++j)
+            if (j < n)
+                load_w(j, at(j));
+        __builtin_amdgcn_sched_barrier(0);
         find_rows();
+#pragma unroll
+        for (int j = 0; j < RING - 1; ++j)
+            if (j < n)
+                load_x(j, at(j));
     }
-    for (; g < end; ++g) {
-        load_w(0, (uint32_t)g * 128);
-        load_x(0, (uint32_t)g * 128);
-        multiply(0);
-    }
+#pragma unroll
+    for (int j = 0; j < RING - 1; ++j)
+        if (j < n)
+            multiply(j);
     if constexpr (WK > 1) {
         __shared__ i32x4 s_part[WN][WK - 1][NSUB * TPW][64];
 #pragma unroll
@@ -386,8 +403,7 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // 1024 cycles of MFMA. Dense 8192 x 14336 x 4096: 433 us, 2.22 POP/s, the matrix
 // units 63% busy at 1.6 GHz (the clock that this load is given; 4.6 POP/s at
 // 2.4 GHz for MFMAs alone). The small tiles are bound by the weight stream:
-// 128 experts of 2048 -> 2 x 768, 64 tokens, 71 us, 5.6 TB/s with every byte
-// fetched once.
+// 128 experts of 2048 -> 2 x 768, 128 tokens, 73 us, 5.6 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 64;
 
@@ -747,13 +763,20 @@ hipError_t launch_tile(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 // tiles (items) that each kernel would have; us on MI355X, operands rotating
 // through more than the 256 MB memory-side cache:
 //   R' <= 32 and few items: the streaming kernel, K split over a workgroup's waves, since
-//     128 x 64 tiles leave CUs idle: dense 16 x 14336 x 4096 16.3 against 23.0 (M x N x K), 1 x 4096 x
+//     128 x 64 tiles leave CUs idle: dense 16 x 14336 x 4096 15.3 against 23.0 (M x N x K), 1 x 4096 x
 //     4096 5.3 against 13.0, 30 x 4096 x 4096 9.9 against 14.0. A wave has as many tiles as leave
-//     most CUs a workgroup: 1 x 4096 x 4096 with one 5.9, two 8.2, four 13.1; 16 x 14336 x 4096
-//     19.6, 16.7, 16.4 (before the default policy)
-//   R' <= 40 (rows spread over experts; 64 where the count is exact): tiles of 64 rows, of 256
+//     most CUs a workgroup: 1 x 4096 x 4096 with one 5.9, two 8.2, four 13.1 (before the default
+//     policy). Where even 64 columns to a workgroup do, two waves of two tiles and half of K each
+//     go before four tiles and a quarter: 8 x 14336 x 4096 14.9 against 16.5, 16 rows 15.3 against
+//     16.1, 16 x 28672 x 4096 31.5 against 30.4
+//   experts with R' <= 5 (SwiGLU), 10 (else): the streaming kernel, half of K to a wave, a quarter
+//     from 2048 on: 128 experts, 2048 -> 2 x 768, 16 tokens 46.5 against 52.6 with 256 x 64 tiles, 64
+//     tokens 69.0 against 72.5, 128 tokens 75.6 against 72.7; 768 -> 2048 26.2 against 29.8, 38.6 against 42.8, 256
+//     tokens 56 against 45; 32 experts of 7168 -> 2 x 2048 with a row each 101 against 118. (Halves for
+//     the long K: 106; quarters for the short one 32.4.)
+//   up to R' = 40 (rows spread over experts; 64 where the count is exact): tiles of 64 rows, of 256
 //     weight rows where that gives 1.5 workgroups per CU, else 128 (128 experts, 2048 -> 2 x 768:
-//     64 tokens 70.9 against 72.7, 256 tokens 73.9 against 79.8; 256 x 128 tiles 78.4 and 80.8)
+//     256 tokens 73.9 against 79.8; 256 x 128 tiles 80.8)
 //   above: 128 rows, with 256 weight rows where that gives 1.5 workgroups per CU (32 experts,
 //     7168 -> 2 x 2048, 64 rows each: 188 against 204 with 128; tiles of 64 rows 266), else 128 (dense
 //     256 x 14336 x 4096 29 against 53), and 64 rows where those leave CUs idle (333 x 2064 x
@@ -777,7 +800,7 @@ hipError_t launch_kind(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
         const bool few4 = items(64, 64) < 192.0, few2 = items(32, 64) < 192.0;
         if (per <= 16.0) {
             if (!few4)
-                return launch_stream<KIND, F32, 1, 4, 4, 2>(g, p, st);
+                return launch_stream<KIND, F32, 1, 2, 2, 2>(g, p, st);
             if constexpr (!SW)
                 if (few2)
                     return launch_stream<KIND, F32, 1, 1, 4, 4>(g, p, st);
@@ -785,6 +808,8 @@ hipError_t launch_kind(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
         }
         return few4 ? launch_stream<KIND, F32, 2, 2, 4, 2>(g, p, st) : launch_stream<KIND, F32, 2, 4, 4, 2>(g, p, st);
     }
+    if (g.offsets && per <= (SW ? 5.0 : 10.0))
+        return g.K < 2048 ? launch_stream<KIND, F32, 1, 2, 2, 2>(g, p, st) : launch_stream<KIND, F32, 1, 2, 4, 4>(g, p, st);
     if (per <= (g.offsets ? 40.0 : 64.0))
         return items(256, 64) >= 384.0 ? launch_tile<KIND, F32, 2, 2, 4, 1, 4>(g, p, st)
                                        : launch_tile<KIND, F32, 2, 1, 2, 2, 5>(g, p, st);
