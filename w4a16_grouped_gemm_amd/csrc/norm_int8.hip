@@ -15,7 +15,7 @@
 //
 // Bound by memory: a row is read once and held in registers between the two
 // reductions (sum of squares, maximum). 8192 x 7168 with the residual, bf16 out,
-// 85 us, 5.5 TB/s; int8 rows of 8192 x 4096 19 us (quantizer), 24 us (norm).
+// 82 us, 5.75 TB/s; int8 rows of 8192 x 4096 19 us (quantizer), 24 us in a run of products.
 // Few rows are a chain of latencies: loads, sum, division, maximum, stores. Rows
 // go through buffer descriptors of their own, so that no access needs a branch:
 // behind branches the compiler does not know how many stores are under way,
