@@ -276,20 +276,23 @@ moe_status moe_w8a8_forward(const moe_shape *shape, const int8_t *x, const float
         g.c = ws.h;
         e = launch_w8_gemm(g, s);
     }
-    // h requantized: the routed rows only, counted on the device
-    if (e == hipSuccess)
-        e = launch_norm(NormLaunch{S, sh.inter, ws.h, nullptr, nullptr, 0.0f, nullptr, nullptr, ws.hq, ws.hs,
-                                   ws.offsets + sh.num_local_experts}, s);
-    if (e == hipSuccess) {
-        W8GemmLaunch g = grouped_args(sh, MOE_GEMM_W2);
+    W8GemmLaunch g = grouped_args(sh, MOE_GEMM_W2);
+    g.offsets = ws.offsets;
+    g.wq = w2_q;
+    g.ws = w2_s;
+    g.c = ws.y;
+    if (quantizes_rows(g)) {
+        g.a_bf16 = ws.h;
+    } else {
         g.a = ws.hq;
         g.as = ws.hs;
-        g.offsets = ws.offsets;
-        g.wq = w2_q;
-        g.ws = w2_s;
-        g.c = ws.y;
-        e = launch_w8_gemm(g, s);
+        // h requantized: the routed rows only, counted on the device
+        if (e == hipSuccess)
+            e = launch_norm(NormLaunch{S, sh.inter, ws.h, nullptr, nullptr, 0.0f, nullptr, nullptr, ws.hq, ws.hs,
+                                       ws.offsets + sh.num_local_experts}, s);
     }
+    if (e == hipSuccess)
+        e = launch_w8_gemm(g, s);
     if (e == hipSuccess)
         e = launch_finalize(sh, ws.y, false, topk_w, ws.inv_perm, out, false, s);
     return from_hip(e);

@@ -8,11 +8,6 @@
 // quantized from the unrounded rows. h is rounded because it is the residual
 // stream that the caller keeps: the norm sees what the next layer will add to.
 //
-// The quotient 127 y / max|y| is rounded correctly near every tie: with r the
-// reciprocal of the maximum, t = 127 y r and one residual step
-// t + fma(-t, max, 127 y) r, so that the many bf16 rows whose values lie
-// exactly between two codes go to the even code, as the definition says.
-//
 // Bound by memory: a row is read once and held in registers between the two
 // reductions (sum of squares, maximum). 8192 x 7168 with the residual, bf16 out,
 // 82 us, 5.75 TB/s; int8 rows of 8192 x 4096 19 us (quantizer), 24 us in a run of products.
@@ -27,30 +22,6 @@
 namespace moe {
 
 namespace {
-
-// A row whose largest magnitude is below 2^-100 counts as zero, so that neither
-// 1 / max overflows nor max / 127 meets a subnormal.
-constexpr float kZeroRow = 0x1p-100f;
-
-// The bits of v from the lane that a DPP control names, 0 where the row mask excludes the lane.
-template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ uint32_t dpp(uint32_t v)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
-}
-
-// A wave's reduction: within quads, half rows and rows, then from row to row, whose last lane has it all. op(x, 0) is x.
-template <class Op>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op)
-{
-    v = op(v, dpp<0xB1>(v));                           // quad_perm [1,0,3,2]
-    v = op(v, dpp<0x4E>(v));                           // quad_perm [2,3,0,1]
-    v = op(v, dpp<0x141>(v));                          // row_half_mirror
-    v = op(v, dpp<0x140>(v));                          // row_mirror
-    v = op(v, dpp<0x142, 0xA>(v));                     // row_bcast:15 to rows 1 and 3
-    v = op(v, dpp<0x143, 0xC>(v));                     // row_bcast:31 to rows 2 and 3
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float x, float *s_red)
@@ -166,10 +137,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
                 top = m > top ? m : top;
             }
         const float amax = __uint_as_float(row_max<TPR>(top, s_red));
-        const bool none = !(amax >= kZeroRow) || !__builtin_isfinite(amax);
-        // a power of two keeps 127 y finite for rows near the end of the range
-        const float f = amax > 0x1p64f ? 0x1p-64f : 1.0f;
-        const float top1 = amax * f, inv = none ? 0.0f : 1.0f / top1;
+        const RowCodes row_codes(amax);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             uint32_t o[2];
@@ -177,17 +145,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
             for (int d = 0; d < 2; ++d) {
                 o[d] = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float y = none ? 0.0f : value(i, 4 * d + j) * (127.0f * f);
-                    const float t0 = y * inv;
-                    const float t1 = __builtin_fmaf(__builtin_fmaf(-t0, top1, y), inv, t0);
-                    o[d] |= ((uint32_t)(int)__builtin_rintf(t1) & 0xFFu) << (8 * j);
-                }
+                for (int j = 0; j < 4; ++j)
+                    o[d] |= row_codes.code(value(i, 4 * d + j)) << (8 * j);
             }
             __builtin_amdgcn_raw_buffer_store_b64(u32x2{o[0], o[1]}, make_rsrc(n.q + at, bytes / 2), off[i] / 2, 0, 0);
         }
         if (lane == 0)
-            n.q_scale[row] = __builtin_isfinite(amax) ? (none ? 0.0f : amax / 127.0f) : __builtin_nanf("");
+            n.q_scale[row] = row_codes.scale;
     }
 }
 
