@@ -212,6 +212,33 @@ def test_layer(T, E, begin, L, k, H, I, mode):
     assert_layer_close(to_np_u16(out), to_np_u16(want), "layer")
 
 
+FUSED = [  # few rows of each expert, I below 2048: the down product quantizes its rows
+    (1, 128, 0, 128, 8, 2048, 768, "uniform"), (16, 64, 0, 64, 6, 2048, 1408, "uniform"), (40, 64, 0, 64, 4, 2048, 1152, "one"),
+    (3, 64, 0, 64, 8, 4096, 1920, "zipf"), (100, 128, 0, 128, 4, 2048, 128, "zipf"), (33, 128, 32, 64, 8, 1024, 1024, "uniform"),
+    (64, 64, 0, 64, 2, 2048, 384, "one"), (90, 256, 16, 32, 16, 2048, 1152, "zipf"), (150, 64, 0, 64, 4, 1024, 640, "uniform"),
+    (17, 1024, 512, 300, 8, 2048, 256, "uniform")]
+
+
+@pytest.mark.parametrize("T,E,begin,L,k,H,I,mode", FUSED)
+def test_layer_of_few_rows(T, E, begin, L, k, H, I, mode):
+    test_layer(T, E, begin, L, k, H, I, mode)
+
+
+@pytest.mark.parametrize("T,I", [(5, 768), (20, 1152), (300, 768)])
+def test_layer_rows_of_nan_and_zero(T, I):
+    """A token's NaN or zero scale reaches its own output only."""
+    from w4a16_grouped_gemm_amd import ops
+    x, ids, w, w13, s13, w2, s2 = layer_inputs(T, 64, 0, 64, 4, 2048, I, "uniform", I + T)
+    xq, xs = ops.int8_quantize(x)
+    want = ops.moe_w8a8_forward(xq, xs, ids, w, w13, s13, w2, s2)
+    xs[1] = float("nan")
+    xs[3] = 0.0
+    out = ops.moe_w8a8_forward(xq, xs, ids, w, w13, s13, w2, s2)
+    assert bool(out[1].isnan().all()) and bool((out[3] == 0).all())
+    keep = torch.tensor([t not in (1, 3) for t in range(T)], device="cuda")
+    assert torch.equal(out[keep], want[keep])
+
+
 def test_layer_with_an_expert_named_twice():
     from w4a16_grouped_gemm_amd import ops
     # the permutation of one workgroup (one and several token ranges) and of many
