@@ -395,3 +395,33 @@ def test_permute_with_an_expert_named_twice(T, E, k):
             assert inv[t, j] == r
             assert r < 0 or (perm[r] // k == t and named[t, perm[r] % k] == e)
     assert (perm[off[-1]:] == -1).all()
+
+
+def test_outputs_are_ordinary_tensors():
+    """Own storage, dense, on the inputs' device; inference tensors in inference mode; also without the short allocation."""
+    from w4a16_grouped_gemm_amd import ops
+    g = gen(9)
+    x = torch.randn(3, 2, 256, generator=g, device="cuda").bfloat16()
+    a, s, w, ws = codes(g, 4, 256), scales(g, 4), codes(g, 32, 256), scales(g, 32)
+    l, gain = torch.randn(5, 16, generator=g, device="cuda"), torch.ones(256, device="cuda").bfloat16()
+
+    def outputs():
+        return [*ops.int8_quantize(x), *ops.add_rms_norm_int8(x, x, gain, with_bf16=True), *ops.route_scored(l, 2),
+                ops.dense_gemm_w8a8(a, s, w, ws), ops.rms_norm(x.view(6, 256), gain)]
+
+    want = outputs()
+    assert [tuple(t.shape) for t in want] == [(3, 2, 256), (3, 2), (3, 2, 256), (3, 2), (3, 2, 256), (3, 2, 256), (5, 2),
+                                              (5, 2), (4, 32), (6, 256)]
+    assert len({t.data_ptr() for t in want}) == len(want)
+    for t in want:
+        assert t.is_contiguous() and t.device == x.device and not t.requires_grad and not t.is_inference()
+    with torch.inference_mode():
+        inside = outputs()
+    short = ops._empty
+    try:
+        ops._empty = lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+        plain = outputs()
+    finally:
+        ops._empty = short
+    for t, i, p in zip(want, inside, plain):
+        assert i.is_inference() and torch.equal(t, i) and torch.equal(t, p)

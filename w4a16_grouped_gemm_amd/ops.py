@@ -595,9 +595,10 @@ def _expect(t, dtype, index, shape, name):
 
 
 def _row_scales(x):
-    """A float32 for each row of x (an int as the size takes 1 us less than a slice of the shape)."""
-    shape = x.shape
-    return torch.empty(shape[0] if len(shape) == 2 else shape[:-1], dtype=torch.float32, device=x.device)
+    """A float32 for each row of x."""
+    if x.dim() == 2:
+        return _empty((x.shape[0],), (1,), torch.float32)
+    return torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
 
 
 def _on_gpu(t, name) -> int:
@@ -634,6 +635,13 @@ _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# A tensor of these sizes, strides (tuples) and dtype on the current device, from the caching allocator as torch.empty's are,
+# without its parsing of arguments and dispatch (0.75 us instead of 1.3)
+_empty = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+_empty = getattr(_empty, "_empty_strided_cuda", None) or (
+    lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
+
+
 def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None = None, score: str = "sigmoid",
                  num_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalize: bool = True,
                  scale: float = 1.0, stream=None):
@@ -653,8 +661,8 @@ def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None 
     _expect(logits, torch.float32, index, (T, E), "logits")
     if bias is not None:
         _expect(bias, torch.float32, index, (E,), "bias")
-    ids = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
-    w = torch.empty_like(ids, dtype=torch.float32)
+    size, stride = (T, top_k), (top_k, 1)
+    ids, w = _empty(size, stride, torch.int32), _empty(size, stride, torch.float32)
     _check((_lib or load_library()).moe_route_scored(
         _shape_ref(T, 128, 128, E, E, top_k), _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale),
         logits.data_ptr(), None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(), _current_stream(index)))
@@ -670,14 +678,15 @@ def _rms_norm(x, residual, weight, eps, sum_out, bf16, int8, stream):
     K = shape[-1] if shape else 0
     _expect(x, torch.bfloat16, index, shape, "x")
     _expect(weight, torch.bfloat16, index, (K,), "weight")
+    size, stride = tuple(shape), x.stride()
     if residual is not None:
         _expect(residual, torch.bfloat16, index, shape, "residual")
         if sum_out is None:
-            sum_out = torch.empty_like(x)
+            sum_out = _empty(size, stride, torch.bfloat16)
         else:
             _expect(sum_out, torch.bfloat16, index, shape, "sum_out")
-    y = torch.empty_like(x) if bf16 else None
-    q = torch.empty_like(x, dtype=torch.int8) if int8 else None
+    y = _empty(size, stride, torch.bfloat16) if bf16 else None
+    q = _empty(size, stride, torch.int8) if int8 else None
     s = _row_scales(x) if int8 else None
     _check((_lib or load_library()).moe_rms_norm(
         x.numel() // K if K else 0, K, x.data_ptr(), None if residual is None else residual.data_ptr(),
@@ -725,7 +734,7 @@ def int8_quantize(x: torch.Tensor, *, stream=None):
             return int8_quantize(x)
     K = x.shape[-1] if x.shape else 0
     _expect(x, torch.bfloat16, index, x.shape, "x")
-    q = torch.empty_like(x, dtype=torch.int8)
+    q = _empty(tuple(x.shape), x.stride(), torch.int8)
     s = _row_scales(x)
     _check((_lib or load_library()).moe_int8_quantize(x.numel() // K if K else 0, K, x.data_ptr(), q.data_ptr(),
                                                       s.data_ptr(), _current_stream(index)))
@@ -749,7 +758,7 @@ def dense_gemm_w8a8(a: torch.Tensor, a_scale: torch.Tensor, wq: torch.Tensor, w_
     _expect(w_scale, torch.float32, index, (N,), "w_scale")
     if out is None:
         dt = _out_dtype(out_dtype)
-        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
+        out = _empty((M, N), (N, 1), out_dtype)
     else:
         dt = _out_dtype(out.dtype)
         _expect(out, out.dtype, index, (M, N), "out")
@@ -785,7 +794,7 @@ def grouped_gemm_w8a8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets
         _expect(a_row_index, torch.int32, index, (rows,), "a_row_index")
     if out is None:
         dt = _out_dtype(out_dtype)
-        out = torch.empty(rows, cols, dtype=out_dtype, device=a.device)
+        out = _empty((rows, cols), (cols, 1), out_dtype)
     else:
         dt = _out_dtype(out.dtype)
         _expect(out, out.dtype, index, (rows, cols), "out")
@@ -823,7 +832,7 @@ def moe_w8a8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Ten
     _expect(w2_q, torch.int8, index, (E_loc, H, I), "w2_q")
     _expect(w2_s, torch.float32, index, (E_loc, H), "w2_s")
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        out = _empty((T, H), (H, 1), torch.bfloat16)
     else:
         _expect(out, torch.bfloat16, index, (T, H), "out")
     lib = _lib or load_library()
@@ -831,7 +840,7 @@ def moe_w8a8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Ten
     if workspace is None:
         # from the caching allocator at every call: it belongs to this stream, or to the graph that is being captured,
         # so no two calls that can overlap share one
-        workspace = torch.empty(max(lib.moe_w8a8_workspace_size(sh), 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty((max(lib.moe_w8a8_workspace_size(sh), 256),), (1,), torch.uint8)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     _check(lib.moe_w8a8_forward(sh, x.data_ptr(), x_scale.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
