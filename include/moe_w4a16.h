@@ -440,6 +440,7 @@ moe_status moe_w8a8_dense_gemm(int32_t M, int32_t N, int32_t K, const int8_t *a,
  * (a [T*k][K], a_scale [T*k]). Kinds and outputs as there (W13_SWIGLU: bf16
  * h = silu(g) * u; W2 / W13_RAW: bf16 or f32); rows >= R of c are untouched.
  * The grid never depends on the counts, no workspace. w_scale 16-byte aligned.
+ * Whatever offsets and a_row_index hold, only these arrays' rows are read and written.
  */
 moe_status moe_grouped_gemm_w8a8(const moe_shape *shape, moe_gemm_kind kind, const int8_t *a, const float *a_scale,
                                  const int32_t *a_row_index, const int32_t *offsets, const int8_t *wq,

@@ -425,3 +425,51 @@ def test_outputs_are_ordinary_tensors():
         ops._empty = short
     for t, i, p in zip(want, inside, plain):
         assert i.is_inference() and torch.equal(t, i) and torch.equal(t, p)
+
+
+LOW, HIGH = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("E", [6, 300])
+@pytest.mark.parametrize("T", [40, 700])
+@pytest.mark.parametrize("hostile", [(LOW, -3, LOW + 7), (LOW, 0, LOW), (-1, LOW, -40), (HIGH, HIGH, HIGH), (LOW, HIGH, HIGH)])
+def test_offsets_that_leave_the_rows(E, T, hostile):
+    """Offsets are the caller's: whatever they hold, only rows of the arrays are read and written. Here two experts have
+    their rows, what follows them goes below 0, past the rows or through the ends of 32 bits."""
+    from w4a16_grouped_gemm_amd import ops
+    say(f"offsets E={E} T={T} {hostile}")
+    g, H, I = gen(E + T), 256, 128
+    a, s, w, ws = codes(g, T, I), scales(g, T), codes(g, E, H, I), scales(g, E, H)
+    n = T // 3
+    offsets = torch.tensor([0, n, 2 * n] + [hostile[i % 3] for i in range(E - 2)], dtype=torch.int32, device="cuda")
+    memory = torch.full((T + 128, H), 7.0, device="cuda")
+    ops.grouped_gemm_w8a8(ops.W2, a, s, offsets, w, ws, num_tokens=T, top_k=1, num_experts=E, out=memory[64:64 + T])
+    out = memory[64:64 + T]
+    assert bool((memory[:64] == 7).all()) and bool((memory[64 + T:] == 7).all())
+    if hostile != (LOW, HIGH, HIGH):                              # else an expert's segment becomes all rows
+        for e in (0, 1):
+            r = slice(e * n, (e + 1) * n)
+            assert near(out[r], dense(a[r], s[r], w[e], ws[e]), F32_REL)
+        if hostile[0] == HIGH:                                    # the third expert's: up to the last row
+            assert near(out[2 * n:], dense(a[2 * n:], s[2 * n:], w[2], ws[2]), F32_REL)
+        else:
+            assert bool((out[2 * n:] == 7).all())
+
+
+@pytest.mark.parametrize("T", [12, 500])
+def test_index_entries_that_leave_the_rows(T):
+    """So are index entries: rows with entries of the array come out right beside others."""
+    from w4a16_grouped_gemm_amd import ops
+    g, E, k, H, I = gen(T), 4, 2, 256, 128
+    x, xs, w, ws = codes(g, T, H), scales(g, T), codes(g, E, 2 * I, H), scales(g, E, 2 * I)
+    perm = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+    bad = torch.arange(T * k, device="cuda") % 5 == 3
+    perm[bad] = torch.tensor([LOW, -1, HIGH, T * k], dtype=torch.int32, device="cuda").repeat(T)[:int(bad.sum())]
+    n = T * k // 4
+    offsets = torch.tensor([0, n, 2 * n, 3 * n, T * k], dtype=torch.int32, device="cuda")
+    out = ops.grouped_gemm_w8a8(ops.W13_RAW, x, xs, offsets, w, ws, num_tokens=T, top_k=k, a_row_index=perm,
+                                out_dtype=torch.float32)
+    token = perm.long().clamp(0, T * k - 1) // k
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        assert near(out[r], dense(x[token[r]], xs[token[r]], w[e], ws[e]), F32_REL)
