@@ -271,12 +271,12 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
         for (int t = 0; t < TPW; ++t)
             acc[s][t] = i32x4{0, 0, 0, 0};
     u32x4 w[RING][TPW][2], x[RING][NSUB][2];
-    auto load_w = [&](int j, uint32_t k) {
+    auto load_w = [&](int j, uint32_t k, uint32_t past = 0) {
 #pragma unroll
         for (int t = 0; t < TPW; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w[j][t][h] = bload16(rw, wo[t] + 64 * h, k);
+                w[j][t][h] = bload16(rw, wo[t] + past + 64 * h, k);
     };
     auto load_x = [&](int j, uint32_t k) {
         if constexpr (!QA)
@@ -341,13 +341,15 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
         }
     };
     auto at = [&](int j) { return (uint32_t)(g + j) * 128; };
-    // the first round's weights set out before the tokens' rows are known
-    if (n >= RING) {
+    // The first round's weights set out before the tokens' rows are known. The waves of a workgroup meet in find_rows,
+    // so there is no branch on n, which differs between them, around it: groups past a wave's last one are loaded from
+    // behind the array, which fetches nothing (a weight offset is below 2^31).
 #pragma unroll
-        for (int j = 0; j < RING; ++j)
-            load_w(j, at(j));
-        __builtin_amdgcn_sched_barrier(0);
-        find_rows();
+    for (int j = 0; j < RING; ++j)
+        load_w(j, at(j), j < n ? 0u : 1u << 31);
+    __builtin_amdgcn_sched_barrier(0);
+    find_rows();
+    if (n >= RING) {
 #pragma unroll
         for (int j = 0; j < RING; ++j)
             load_x(j, at(j));
@@ -369,12 +371,6 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
         }
         g += RING;
     } else {
-#pragma unroll
-        for (int j = 0; j < RING - 1; ++j)
-            if (j < n)
-                load_w(j, at(j));
-        __builtin_amdgcn_sched_barrier(0);
-        find_rows();
 #pragma unroll
         for (int j = 0; j < RING - 1; ++j)
             if (j < n)
