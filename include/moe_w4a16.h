@@ -226,8 +226,8 @@ size_t moe_permute_workspace_size(const moe_shape *shape);
  *                x_perm bf16 [T*k][H], row r = x[perm[r] / k] (rows >= R
  *                untouched)
  * Bit-exact and deterministic (no atomics decide a position). A token that
- * names a local expert twice has one row for it (counted once, perm holds one
- * of the slots), and both slots' inv_perm give that row.
+ * names a local expert twice has one row for it (counted once, perm holds the
+ * last of the slots), and both slots' inv_perm give that row.
  * workspace: device memory of moe_permute_workspace_size(shape) bytes,
  * 4-byte aligned (NULL if that is 0); smaller -> MOE_ERR_WORKSPACE.
  */

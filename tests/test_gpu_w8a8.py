@@ -473,3 +473,23 @@ def test_index_entries_that_leave_the_rows(T):
     for e in range(E):
         r = slice(int(offsets[e]), int(offsets[e + 1]))
         assert near(out[r], dense(x[token[r]], xs[token[r]], w[e], ws[e]), F32_REL)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 16, 16), (5, 4, 3), (40, 7, 7), (64, 128, 16), (93, 11, 11), (100, 1000, 10), (128, 8, 8),
+                                   (300, 1024, 3), (380, 8, 4), (500, 8, 4), (3000, 64, 16)])
+def test_permute_keeps_the_last_slot_of_a_row(T, E, k):
+    """The row of a token that names an expert more than once holds the last of those slots, in every variant and at
+    every call."""
+    from w4a16_grouped_gemm_amd import ops
+    say(f"permute T={T} E={E} k={k}, the slot of a shared row")
+    ids = torch.randint(-1, E + 1, (T, k), generator=gen(T + k), device="cuda", dtype=torch.int32)
+    first = ops.permute(ids, E)
+    for _ in range(5):
+        again = ops.permute(ids, E)
+        assert all(torch.equal(a, b) for a, b in zip(first[:4], again[:4]))
+    offsets, perm, inv = (t.cpu().numpy() for t in first[1:4])
+    want = np.full(T * k, -1)
+    for slot in range(T * k):                                     # in order, so the last one stays
+        if inv[slot // k, slot % k] >= 0:
+            want[inv[slot // k, slot % k]] = slot
+    assert np.array_equal(perm, want) and (want[:offsets[-1]] >= 0).all()

@@ -391,7 +391,8 @@ __global__ __launch_bounds__(kPermThreads) void permute_kernel(
 // Few slots and experts (at most 1024 each): a thread per slot, and per expert.
 // The same tables as permute_kernel's, whose one-chunk path gives a thread a
 // token with its k slots one after another; 16 tokens of top-8 over 128 experts
-// 7.7 -> 2.6 us.
+// 7.7 -> 2.6 us. The slots of a token that names an expert twice share a row; its
+// entry is the last of them, as where one thread writes them in turn.
 __global__ __launch_bounds__(1024) void permute_small_kernel(int T, int k, int begin, int E, int words,
                                                              const int32_t *__restrict__ ids,
                                                              int32_t *__restrict__ counts,
@@ -400,12 +401,14 @@ __global__ __launch_bounds__(1024) void permute_small_kernel(int T, int k, int b
                                                              int32_t *__restrict__ inv_perm)
 {
     __shared__ int s_off[kMaxExperts];
+    __shared__ int s_slot[1024];                         // [S]: slot of a row, -1 past the last row
     __shared__ int s_wave_tot[1024 / 64];
     extern __shared__ uint32_t s_dyn[];                  // [E][words]: bit t of expert e <=> token t routed to it
     const int tid = threadIdx.x, S = T * k, waves = blockDim.x >> 6;
     int e = tid < S ? ids[tid] - begin : -1;
     for (int i = tid; i < E * words; i += blockDim.x)
         s_dyn[i] = 0u;
+    s_slot[tid] = -1;
     e = e >= 0 && e < E ? e : -1;
     const int t = tid / k;
     __syncthreads();
@@ -441,12 +444,13 @@ __global__ __launch_bounds__(1024) void permute_small_kernel(int T, int k, int b
             row = s_off[e] + __popc(s_dyn[e * words + (t >> 5)] & ((1u << (t & 31)) - 1u));
             for (int w = 0; w < t >> 5; ++w)
                 row += __popc(s_dyn[e * words + w]);
-            perm[row] = tid;
+            atomicMax(&s_slot[row], tid);
         }
         inv_perm[tid] = row;
     }
-    for (int r = R + tid; r < S; r += blockDim.x)
-        perm[r] = -1;
+    __syncthreads();
+    if (tid < S)
+        perm[tid] = s_slot[tid];
 }
 
 // Parallel path, step 1: expert histogram of each workgroup's token range
