@@ -781,6 +781,8 @@ def grouped_gemm_w8a8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets
     if wq.dim() != 3:
         raise ValueError("wq must be [E, N, K]")
     E_loc, N, K = wq.shape
+    if kind != W2 and N % 2:
+        raise ValueError("wq must have a gate row and an up row for each column, an even number")
     H, I = (N, K) if kind == W2 else (K, N // 2)
     cols = I if kind == W13_SWIGLU else N
     rows = num_tokens * top_k
