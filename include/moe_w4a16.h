@@ -406,7 +406,9 @@ moe_status moe_w4a4_forward(const moe_shape *shape, const uint16_t *x, const flo
  * rint is to the nearest, ties to the even code, of the exact quotient up to
  * one binary32 rounding. A row whose largest |v| is below 2^-100 gets codes
  * and scale 0; a row with a NaN or an infinity gets codes 0 and a NaN scale,
- * so that whatever is computed from it is NaN.
+ * so that whatever is computed from it is NaN. h may hold any finite values:
+ * squares that leave binary32's range are those of h times a power of two. A
+ * row of zeros with eps 0 gives NaN (0 / 0).
  *   x, residual, sum, y  bf16 [rows][K]; weight bf16 [K]
  *   q int8 [rows][K], q_scale f32 [rows]
  * At least one of y and q. eps >= 0. Fewer than 2^25 rows for K <= 1024, 2^23

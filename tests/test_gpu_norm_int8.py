@@ -161,3 +161,43 @@ def test_refuses_a_tensor_without_dimensions():
     for call in (lambda: ops.rms_norm(x, w), lambda: ops.add_rms_norm_int8(x, x, w), lambda: ops.int8_quantize(x)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("K", [8, 512, 1032, 2048, 7168, 16384, 40960])
+@pytest.mark.parametrize("rows", [3, 1100])
+@pytest.mark.parametrize("res", [False, True])
+def test_rows_whose_squares_leave_binary32(rows, K, res):
+    """Finite rows have a norm of order one however large or small they are: among ordinary rows some whose squares
+    are infinite (the largest bf16 values among them), none at all (bf16 subnormals among them) or subnormal. rstd of
+    rows above 2^126 is subnormal itself, off by up to 2^-22 = 4 u more, which the bound of 64 u has room for."""
+    from w4a16_grouped_gemm_amd import ops
+    if rows * K > 1 << 24:
+        rows = 300
+    say(f"norm of extreme rows {rows}x{K} residual={res}")
+    x, r, w = inputs(rows, K, rows + K)
+    power = torch.tensor([0.0, 62, 64, 66, 100, 122, -50, -54, -60, -64, -70, -100, -120, -128])
+    scale = 2.0 ** power[torch.arange(rows) % 14].double()
+    x = (x.double().clamp(-15, 15) * scale[:, None]).bfloat16()
+    r = (r.double().clamp(-15, 15) * scale[:, None]).bfloat16() if res else None
+    x[0] = 0
+    x[0, K // 2] = 3.0 * 2.0 ** 125                   # one value alone, a large and a small one
+    x[2] = 0
+    x[2, K - 1] = -2.0 ** -133
+    if res:
+        r[0] = 0
+        r[2] = 0
+    for eps in (0.0, 1e-6, 2.0 ** -130):
+        h, v = reference(x, r, w, eps)
+        assert h.isfinite().all() and v.isfinite().all()
+        if res:
+            q, sc, s2, y = ops.add_rms_norm_int8(x.cuda(), r.cuda(), w.cuda(), eps=eps, with_bf16=True)
+            y2, _ = ops.add_rms_norm(x.cuda(), r.cuda(), w.cuda(), eps=eps)
+            assert torch.equal(s2.cpu(), h)
+        else:
+            q, sc, y = ops.rms_norm_int8(x.cuda(), w.cuda(), eps=eps, with_bf16=True)
+            y2 = ops.rms_norm(x.cuda(), w.cuda(), eps=eps)
+        assert torch.equal(y, y2)
+        assert near(y, v, 2.0 ** -8 + 2 * V)
+        some = v.abs().amax(-1) >= 2.0 ** -100        # a row below that counts as zero
+        check_codes(q[some.cuda()], sc[some.cuda()], v[some])
+        assert (q[~some.cuda()] == 0).all() and (sc[~some.cuda()] == 0).all()

@@ -7,6 +7,7 @@
 // All in binary32; y is rounded to bf16 only where it is stored as bf16, so q is
 // quantized from the unrounded rows. h is rounded because it is the residual
 // stream that the caller keeps: the norm sees what the next layer will add to.
+// A row whose squares binary32 does not hold is done apart (scaled_row).
 //
 // Bound by memory: a row is read once and held in registers between the two
 // reductions (sum of squares, maximum). 8192 x 7168 with the residual, bf16 out,
@@ -63,6 +64,77 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float *s_red)
     return v;
 }
 
+// A mean of squares plus eps from which the norm is not taken: past binary32's range (or NaN), or so small that
+// squares lost bits, or all of them.
+__device__ __forceinline__ bool out_of_range(float ms) { return !(ms >= 0x1p-100f && ms < __builtin_inff()); }
+
+// The norm of a row of finite values out of binary32's range for squares: the squares are those of the row times a
+// power of two f, which keeps any bf16 row's within it. Small rows are taken times f, since their rstd may be too
+// large (f times the row is exact); of large ones rstd is, which may make it subnormal (off by 2^-22). Read again
+// from memory, three times, in loops, so that ordinary rows do not pay for it with registers (from the registers that
+// hold the row, 8192 x 7168 to int8 took 40 us instead of 34).
+template <int TPR, bool RES, bool Y, bool Q>
+__device__ __forceinline__ void scaled_row(const NormLaunch &n, long long row, int lane, bool small, float *s_red)
+{
+    const size_t at = (size_t)row * n.K;
+    const uint32_t bytes = (uint32_t)n.K * 2;
+    // with a residual this thread has just stored h; y may stand in x's place, so it is stored after the last read
+    const __amdgpu_buffer_rsrc_t rh = make_rsrc((RES ? n.sum : n.x) + at, bytes), rg = make_rsrc(n.weight, bytes);
+    const float f = small ? 0x1p90f : 0x1p-73f;
+    float sq = 0.0f;
+#pragma unroll 1
+    for (uint32_t o = lane * 16; o < bytes; o += TPR * 16) {
+        const u32x4 h = bload16(rh, o, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = bf16_to_f32(h[j] & 0xFFFFu) * f, b = bf16_to_f32(h[j] >> 16) * f;
+            sq = __builtin_fmaf(a, a, sq);
+            sq = __builtin_fmaf(b, b, sq);
+        }
+    }
+    const float rs = 1.0f / sqrtf(row_sum<TPR>(sq, s_red) / (float)n.K + n.eps * f * f);
+    const float rstd = small ? rs : rs * f, hf = small ? f : 1.0f;
+    auto load_values = [&](uint32_t o, float (&v)[8]) {
+        const u32x4 h = bload16(rh, o, 0), g = bload16(rg, o, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_to_f32(h[j] & 0xFFFFu) * hf * rstd * bf16_to_f32(g[j] & 0xFFFFu);
+            v[2 * j + 1] = bf16_to_f32(h[j] >> 16) * hf * rstd * bf16_to_f32(g[j] >> 16);
+        }
+    };
+    uint32_t top = 0;
+    if constexpr (Q) {
+#pragma unroll 1
+        for (uint32_t o = lane * 16; o < bytes; o += TPR * 16) {
+            float v[8];
+            load_values(o, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
+        top = row_max<TPR>(top, s_red);
+    }
+    const RowCodes row_codes(__uint_as_float(top));
+#pragma unroll 1
+    for (uint32_t o = lane * 16; o < bytes; o += TPR * 16) {
+        float v[8];
+        load_values(o, v);
+        if constexpr (Q) {
+            uint32_t c[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                c[j >> 2] |= row_codes.code(v[j]) << (8 * (j & 3));
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, make_rsrc(n.q + at, bytes / 2), o / 2, 0, 0);
+        }
+        if constexpr (Y)
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
+                                                         bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])},
+                                                   make_rsrc(n.y + at, bytes), o, 0, 0);
+    }
+    if (Q && lane == 0)
+        n.q_scale[row] = row_codes.scale;
+}
+
 // TPR threads per row (64: one wave, four rows to a workgroup; else the whole
 // workgroup), each with VPT vectors of 8 values at stride TPR.
 template <int TPR, int VPT, bool RES, bool NORM, bool Y, bool Q>
@@ -70,6 +142,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
 {
     __shared__ float s_red[TPR / 64];
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    // a row that scaled_row does: behind the stores, which it then overwrites, where its row is still there (a branch
+    // before them costs a single row 0.1 us), else instead of them (y in place of x)
+    constexpr bool kFirst = Y && !RES;
     const int lane = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * RPB + uniform(threadIdx.x / TPR);
     if (row >= (n.rows_dev ? n.rows_dev[0] : n.rows))
@@ -85,6 +160,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
         xv[i] = bload16(rx, off[i], 0);
         if constexpr (RES)
             rv[i] = bload16(make_rsrc(n.residual + at, bytes), off[i], 0);
+        __builtin_amdgcn_sched_barrier(0);             // in the order of their use (1 x 7168 2.90 us in another)
     }
     if constexpr (NORM)
 #pragma unroll
@@ -109,9 +185,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
                 sq = __builtin_fmaf(b, b, sq);
             }
     }
-    float rstd = 1.0f;
-    if constexpr (NORM)
-        rstd = 1.0f / sqrtf(row_sum<TPR>(sq, s_red) / (float)n.K + n.eps);
+    float ms = 1.0f, rstd = 1.0f;
+    if constexpr (NORM) {
+        ms = row_sum<TPR>(sq, s_red) / (float)n.K + n.eps;
+        if (kFirst && __builtin_expect(out_of_range(ms), 0)) {   // all threads of a row alike
+            scaled_row<TPR, RES, Y, Q>(n, row, lane, ms < 0x1p-100f, s_red);
+            return;
+        }
+        rstd = 1.0f / sqrtf(ms);
+    }
     auto value = [&](int i, int j) {                   // element j of vector i
         const uint32_t h = j & 1 ? xv[i][j >> 1] >> 16 : xv[i][j >> 1] & 0xFFFFu;
         if constexpr (!NORM)
@@ -153,6 +235,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormLaunch 
         if (lane == 0)
             n.q_scale[row] = row_codes.scale;
     }
+    if (NORM && !kFirst && __builtin_expect(out_of_range(ms), 0))
+        scaled_row<TPR, RES, Y, Q>(n, row, lane, ms < 0x1p-100f, s_red);
 }
 
 template <int TPR, int VPT>
