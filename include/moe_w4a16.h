@@ -478,7 +478,8 @@ moe_status moe_w8a8_forward(const moe_shape *shape, const int8_t *x, const float
  *   topk_w = s of the slot's expert (without b), divided by the sum of the k
  *   chosen s if renormalize (0 where that sum is 0), times scale
  * An expert whose logit is -inf (switched off) or whose c is NaN is chosen after
- * all others, with weight 0.
+ * all others (those with a c of -inf too), with weight 0, and counts as -inf in
+ * its group's score.
  *   logits f32 [T][E_g], bias f32 [E_g] -> topk_ids int32 [T][k], topk_w f32 [T][k]
  * G divides E_g, G <= 64, 1 <= topk_groups <= G, group_top <= E_g/G,
  * top_k <= topk_groups * E_g/G.

@@ -179,3 +179,44 @@ def test_refuses_no_slots(k):
     from w4a16_grouped_gemm_amd import ops
     with pytest.raises(ValueError):
         ops.route_scored(torch.zeros(4, 32, device="cuda"), k)
+
+
+@pytest.mark.parametrize("E,k,G,kept,top", [(16, 16, 1, 1, 1), (32, 12, 4, 2, 1), (32, 12, 4, 2, 2), (128, 16, 1, 1, 1),
+                                            (256, 16, 8, 2, 2), (160, 16, 8, 2, 1), (512, 16, 1, 1, 1), (1000, 16, 8, 2, 2)])
+@pytest.mark.parametrize("T", [5, 4100])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_a_bias_of_minus_infinity_comes_before_what_is_switched_off(E, k, G, kept, top, T, score):
+    """Experts that are left: first by c, then those whose bias alone is -inf, then the masked ones (logit -inf, or c
+    NaN); lower index first in each. In its group's score a masked expert counts as -inf."""
+    from w4a16_grouped_gemm_amd import ops
+    say(f"route_scored -inf bias E={E} k={k} G={G} kept={kept} top={top} T={T} {score}")
+    rng = np.random.default_rng(E + k)
+    l = (rng.standard_normal((7, E)) * 1.5).astype(np.float32)
+    l[:, rng.permutation(E)[:E // 3]] = -np.inf
+    l[3, ::2] = np.nan
+    l[4] = -np.inf
+    b = np.full(E, -np.inf, np.float32)
+    b[rng.permutation(E)[:max(2, k // 4)]] = 0.25
+    b[1] = np.nan
+    rows = np.arange(T) % 7
+    ids, w = run(np.ascontiguousarray(l[rows]), b, k, score=score, num_groups=G, topk_groups=kept, group_top=top,
+                 renormalize=False, scale=1.5)
+    d = l.astype(np.float64)
+    for t in range(7):
+        with np.errstate(all="ignore"):
+            p = 1 / (1 + np.exp(-d[t])) if score == "sigmoid" else np.exp(d[t] - np.nanmax(d[t]))
+            s = (p if score == "sigmoid" else p / np.nansum(p)).astype(np.float32)
+            c = s + b
+        off = np.isneginf(l[t]) | np.isnan(c)
+        c[off] = -np.inf
+        allowed = range(E)
+        if G > 1:
+            best = -np.sort(-c.reshape(G, -1), axis=1)
+            g = best[:, 0] if top == 1 else best[:, 0] + best[:, 1]
+            groups = sorted(range(G), key=lambda i: (-g[i], i))[:kept]
+            allowed = [e for e in range(E) if e // (E // G) in groups]
+        want = sorted(allowed, key=lambda e: (off[e], -c[e], e))[:k]
+        share = np.where(off, 0, s.astype(np.float64) * 1.5)[want]
+        for i in np.flatnonzero(rows == t):
+            assert np.array_equal(ids[i], want), t
+            assert (np.abs(w[i] - share) <= 4 * 2.0 ** -24 * share + 2.0 ** -148).all()

@@ -36,8 +36,10 @@ namespace {
 constexpr int kScoredWaves = 4;
 constexpr int kManyTokens = 4096;        // with 16 lanes per token a wave for each SIMD
 
-// Key of an expert that may be chosen only after all others (masked) and of one that may not be chosen.
-constexpr uint32_t kMaskedKey = 0x007FFFFFu;           // ordered_bits(-inf): below every finite value's
+// Key of an expert that may be chosen only after all others (masked): below that of -inf, which a bias can make of c;
+// in its group's score it counts as -inf. And of one that may not be chosen.
+constexpr uint32_t kLowestKey = 0x007FFFFFu;           // ordered_bits(-inf)
+constexpr uint32_t kMaskedKey = kLowestKey - 1;
 constexpr uint32_t kNoKey = 0u;
 
 // The maximum of the TL lanes that hold a token, in each of them.
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
     }
     if constexpr (GROUPS > 0) {
         const int G = r.num_groups, size = E / G;
-        uint32_t a = 0, b2 = 0;                        // the two largest keys of a group
+        uint32_t a = kLowestKey, b2 = kLowestKey;      // the two largest keys of a group
         int my_g, gl;                                  // the lane's group; lanes from one group's holder to the next's
         if constexpr (GROUPS == 1) {
 #pragma unroll
@@ -237,6 +239,7 @@ __global__ __launch_bounds__(kScoredWaves * 64) void route_scored_kernel(
                 s_key[wave][e0 + i] = key[i];
             __syncthreads();
             if (lane < G)                              // lane g holds group g
+#pragma unroll 4
                 for (int i = 0; i < size; ++i)
                     merge_top2(a, b2, s_key[wave][lane * size + i], 0u);
             gl = 1;
