@@ -60,3 +60,46 @@ def test_grouped_refuses_other_shapes(library):
         with pytest.raises(ValueError):
             ops.grouped_gemm_w8a8(ops.W13_SWIGLU, *args, **{**kw, **more})
     assert not library.calls
+
+
+def routers(library):
+    return [args[1]._obj for name, args in library.calls if name == "moe_route_scored"]
+
+
+def test_a_router_goes_by_values_not_by_the_objects_that_held_them(library):
+    """A number given as a tensor of no dimensions is read at each call, and -0.0 is another factor than 0.0."""
+    logits = torch.zeros(3, 16)
+    scale, groups, k = torch.tensor(2.0), torch.tensor(4), torch.tensor(2)
+    ops.route_scored(logits, k, scale=scale, num_groups=groups, topk_groups=2)
+    scale.fill_(3.0)
+    groups.fill_(2)
+    k.fill_(3)
+    ids, w = ops.route_scored(logits, k, scale=scale, num_groups=groups, topk_groups=2)
+    assert ids.shape == w.shape == (3, 3)
+    first, second = routers(library)
+    assert (first.scale, first.num_groups, second.scale, second.num_groups) == (2.0, 4, 3.0, 2)
+    shapes = [args[0]._obj for _, args in library.calls]
+    assert [s.top_k for s in shapes] == [2, 3]
+    for factor in (0.0, -0.0, 0.0):
+        ops.route_scored(logits, 2, scale=factor)
+    assert [str(r.scale) for r in routers(library)[2:]] == ["0.0", "-0.0", "0.0"]
+
+
+def test_a_shape_goes_by_values_too(library):
+    a, s, off = torch.zeros(6, 128, dtype=torch.int8), torch.ones(6), torch.zeros(3, dtype=torch.int32)
+    w, ws = torch.zeros(2, 256, 128, dtype=torch.int8), torch.ones(2, 256)
+    T, E = torch.tensor(3), torch.tensor(2)
+    ops.grouped_gemm_w8a8(ops.W13_SWIGLU, a, s, off, w, ws, num_tokens=T, top_k=2, num_experts=E)
+    T.fill_(6)
+    E.fill_(8)
+    ops.grouped_gemm_w8a8(ops.W13_SWIGLU, a, s, off, w, ws, num_tokens=T, top_k=1, num_experts=E)
+    begin, E = torch.tensor(0), torch.tensor(4)
+    x, ids, tw = torch.zeros(6, 128, dtype=torch.int8), torch.zeros(6, 2, dtype=torch.int32), torch.ones(6, 2)
+    w2, w2s = torch.zeros(2, 128, 128, dtype=torch.int8), torch.ones(2, 128)
+    layer = (x, s, ids, tw, w, ws, w2, w2s)
+    space = torch.empty(256, dtype=torch.uint8)
+    ops.moe_w8a8_forward(*layer, num_experts=E, expert_begin=begin, workspace=space)
+    begin.fill_(2)
+    ops.moe_w8a8_forward(*layer, num_experts=E, expert_begin=begin, workspace=space)
+    got = [args[0]._obj for name, args in library.calls]
+    assert [(s.num_tokens, s.num_experts, s.expert_begin) for s in got] == [(3, 2, 0), (6, 8, 0), (6, 4, 0), (6, 4, 2)]

@@ -13,6 +13,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
+import operator
 import os
 import threading
 
@@ -615,17 +617,18 @@ def _out_dtype(dtype):
     raise ValueError("out dtype must be bfloat16 or float32")
 
 
+# Structures by the values of their fields: callers pass plain numbers (of a tensor, its value at the time of the call)
 @functools.lru_cache(maxsize=1024)
 def _shape_ref(*args):
     return ctypes.byref(make_shape(*args))
 
 
 @functools.lru_cache(maxsize=256)
-def _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale):
+def _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale, sign):
+    # sign: what tells 0.0 from -0.0, which are the same key
     if score not in ("softmax", "sigmoid"):
         raise ValueError("score must be 'softmax' or 'sigmoid'")
-    return ctypes.byref(Router(int(score == "sigmoid"), int(num_groups), int(topk_groups), int(group_top),
-                               int(bool(renormalize)), float(scale)))
+    return ctypes.byref(Router(int(score == "sigmoid"), num_groups, topk_groups, group_top, int(renormalize), scale))
 
 
 # The current device without the check that the GPU is in use (its tensors are), and the current stream's handle without
@@ -655,6 +658,7 @@ def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None 
         with there:
             return route_scored(logits, top_k, bias=bias, score=score, num_groups=num_groups, topk_groups=topk_groups,
                                 group_top=group_top, renormalize=renormalize, scale=scale)
+    top_k, scale = operator.index(top_k), float(scale)
     if logits.dim() != 2 or top_k < 1:
         raise ValueError("logits must be [T, E] and top_k at least 1")
     T, E = logits.shape
@@ -664,7 +668,9 @@ def route_scored(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None 
     size, stride = (T, top_k), (top_k, 1)
     ids, w = _empty(size, stride, torch.int32), _empty(size, stride, torch.float32)
     _check((_lib or load_library()).moe_route_scored(
-        _shape_ref(T, 128, 128, E, E, top_k), _router_ref(score, num_groups, topk_groups, group_top, renormalize, scale),
+        _shape_ref(T, 128, 128, E, E, top_k),
+        _router_ref(score, int(num_groups), int(topk_groups), int(group_top), bool(renormalize), scale,
+                    scale or math.copysign(1.0, scale)),
         logits.data_ptr(), None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(), _current_stream(index)))
     return ids, w
 
@@ -785,6 +791,7 @@ def grouped_gemm_w8a8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets
         raise ValueError("wq must have a gate row and an up row for each column, an even number")
     H, I = (N, K) if kind == W2 else (K, N // 2)
     cols = I if kind == W13_SWIGLU else N
+    num_tokens, top_k = operator.index(num_tokens), operator.index(top_k)
     rows = num_tokens * top_k
     a_rows = rows if a_row_index is None else num_tokens
     _expect(a, torch.int8, index, (a_rows, K), "a")
@@ -801,9 +808,9 @@ def grouped_gemm_w8a8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets
         dt = _out_dtype(out.dtype)
         _expect(out, out.dtype, index, (rows, cols), "out")
     _check((_lib or load_library()).moe_grouped_gemm_w8a8(
-        _shape_ref(num_tokens, H, I, num_experts or E_loc, E_loc, top_k, 0, 0), kind, a.data_ptr(), a_scale.data_ptr(),
-        None if a_row_index is None else a_row_index.data_ptr(), offsets.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
-        out.data_ptr(), dt, _current_stream(index)))
+        _shape_ref(num_tokens, H, I, operator.index(num_experts or E_loc), E_loc, top_k, 0, 0), kind, a.data_ptr(),
+        a_scale.data_ptr(), None if a_row_index is None else a_row_index.data_ptr(), offsets.data_ptr(), wq.data_ptr(),
+        w_scale.data_ptr(), out.data_ptr(), dt, _current_stream(index)))
     return out
 
 
@@ -838,7 +845,8 @@ def moe_w8a8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Ten
     else:
         _expect(out, torch.bfloat16, index, (T, H), "out")
     lib = _lib or load_library()
-    sh = _shape_ref(T, H, I, num_experts or expert_begin + E_loc, E_loc, k, expert_begin, 0)
+    begin = operator.index(expert_begin)
+    sh = _shape_ref(T, H, I, operator.index(num_experts or begin + E_loc), E_loc, k, begin, 0)
     if workspace is None:
         # from the caching allocator at every call: it belongs to this stream, or to the graph that is being captured,
         # so no two calls that can overlap share one
