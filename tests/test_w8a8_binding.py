@@ -103,3 +103,31 @@ def test_a_shape_goes_by_values_too(library):
     ops.moe_w8a8_forward(*layer, num_experts=E, expert_begin=begin, workspace=space)
     got = [args[0]._obj for name, args in library.calls]
     assert [(s.num_tokens, s.num_experts, s.expert_begin) for s in got] == [(3, 2, 0), (6, 8, 0), (6, 4, 0), (6, 4, 2)]
+
+
+class Stream:
+    """Stands for a torch.cuda.Stream of a device."""
+
+    def __init__(self, index):
+        self.device_index = index
+        self.device = torch.device("cuda", index)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """What ran there instead was the current stream of the tensors' device, without a word."""
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: ("on", s))
+    monkeypatch.setattr(ops, "_on_gpu", lambda t, name: 0)
+    here, other = Stream(0), Stream(1)
+    assert ops._elsewhere(0, here) == ("on", here)
+    x, w = torch.zeros(2, 128, dtype=torch.bfloat16), torch.ones(128, dtype=torch.bfloat16)
+    q, s, ids = torch.zeros(2, 128, dtype=torch.int8), torch.ones(2), torch.zeros(2, 1, dtype=torch.int32)
+    off, w3, ws3 = torch.zeros(2, dtype=torch.int32), torch.zeros(1, 256, 128, dtype=torch.int8), torch.ones(1, 256)
+    for call in (lambda: ops.rms_norm(x, w, stream=other), lambda: ops.add_rms_norm(x, x, w, stream=other),
+                 lambda: ops.rms_norm_int8(x, w, stream=other), lambda: ops.add_rms_norm_int8(x, x, w, stream=other),
+                 lambda: ops.int8_quantize(x, stream=other), lambda: ops.route_scored(x.float(), 2, stream=other),
+                 lambda: ops.dense_gemm_w8a8(q, s, w3[0], ws3[0], stream=other),
+                 lambda: ops.grouped_gemm_w8a8(ops.W13_SWIGLU, q, s, off, w3, ws3, num_tokens=2, top_k=1, stream=other),
+                 lambda: ops.moe_w8a8_forward(q, s, ids, ids.float(), w3, ws3, w3, ws3, stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()

@@ -582,6 +582,8 @@ def _elsewhere(index: int, stream):
         return None if index == _current_device() else torch.cuda.device(index)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream is one of cuda:{stream.device_index}, the tensors are on cuda:{index}")
     return torch.cuda.stream(stream)
 
 
