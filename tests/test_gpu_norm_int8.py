@@ -201,3 +201,15 @@ def test_rows_whose_squares_leave_binary32(rows, K, res):
         some = v.abs().amax(-1) >= 2.0 ** -100        # a row below that counts as zero
         check_codes(q[some.cuda()], sc[some.cuda()], v[some])
         assert (q[~some.cuda()] == 0).all() and (sc[~some.cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("rows,K", [(1025, 2048), (1024, 1032)])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_of_many_rows(rows, K, res):
+    """A wave to a row of more than 1024 values, which many rows get."""
+    test_norm(rows, K, res)
+
+
+@pytest.mark.parametrize("rows,K", [(3, 7168), (2, 4104)])
+def test_quantizer_of_more_row_lengths(rows, K):
+    test_quantizer_is_exact(rows, K)

@@ -220,3 +220,11 @@ def test_a_bias_of_minus_infinity_comes_before_what_is_switched_off(E, k, G, kep
         for i in np.flatnonzero(rows == t):
             assert np.array_equal(ids[i], want), t
             assert (np.abs(w[i] - share) <= 4 * 2.0 ** -24 * share + 2.0 ** -148).all()
+
+
+@pytest.mark.parametrize("T,E,k,G,kept,top", [(9, 200, 8, 1, 1, 1), (7, 256, 16, 1, 1, 1), (4, 1000, 16, 1, 1, 1),
+                                              (5, 360, 6, 8, 3, 2), (3, 512, 9, 2, 1, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_of_more_sizes(T, E, k, G, kept, top, score):
+    """The forms of the kernel that no size above reaches: many experts without groups, or in groups of any size."""
+    test_route(T, E, k, G, kept, top, score)

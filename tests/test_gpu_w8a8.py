@@ -493,3 +493,14 @@ def test_permute_keeps_the_last_slot_of_a_row(T, E, k):
         if inv[slot // k, slot % k] >= 0:
             want[inv[slot // k, slot % k]] = slot
     assert np.array_equal(perm, want) and (want[:offsets[-1]] >= 0).all()
+
+
+VARIANTS = [  # shapes for the kernel variants that no shape above reaches
+    (256, 128, 0, 128, 8, 1024, 768, "uniform"),                  # 256 x 64 tiles, in all three kinds
+    (24, 4, 0, 4, 4, 256, 256, "uniform"),                        # the streaming SwiGLU product of two token subtiles,
+    (24, 4, 0, 4, 4, 256, 2048, "uniform")]                       # of two tiles a wave and of four
+
+
+@pytest.mark.parametrize("T,E,begin,L,k,H,I,mode", VARIANTS)
+def test_grouped_in_the_other_variants(T, E, begin, L, k, H, I, mode):
+    test_grouped(T, E, begin, L, k, H, I, mode)
