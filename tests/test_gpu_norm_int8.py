@@ -213,3 +213,40 @@ def test_norm_of_many_rows(rows, K, res):
 @pytest.mark.parametrize("rows,K", [(3, 7168), (2, 4104)])
 def test_quantizer_of_more_row_lengths(rows, K):
     test_quantizer_is_exact(rows, K)
+
+
+@pytest.mark.parametrize("rows,K", [(9, 512), (5, 2048), (1030, 2048), (4, 7168), (3, 40960)])
+@pytest.mark.parametrize("extreme", [False, True])
+def test_outputs_in_place_of_inputs(rows, K, extreme):
+    """The C entry's in-place forms: y over x, the sum over the residual and y over x, the sum over x and y over the
+    residual; rows out of binary32's range for squares are read again, so they must not be overwritten first."""
+    import ctypes
+
+    from w4a16_grouped_gemm_amd import ops
+    say(f"norm in place {rows}x{K} extreme={extreme}")
+    lib = ops.load_library()
+    x, r, w = inputs(rows, K, rows + 3 * K)
+    if extreme:
+        scale = 2.0 ** torch.tensor([0.0, 66, 120, -70, -125])[torch.arange(rows) % 5].double()[:, None]
+        x, r = (x.double().clamp(-15, 15) * scale).bfloat16(), (r.double().clamp(-15, 15) * scale).bfloat16()
+    wd = w.cuda()
+
+    def call(xd, rd, sd, yd):
+        q = torch.empty(rows, K, dtype=torch.int8, device="cuda")
+        s = torch.empty(rows, device="cuda")
+        p = [None if t is None else t.data_ptr() for t in (xd, rd, wd)]
+        assert lib.moe_rms_norm(rows, K, *p, 1e-20, None if sd is None else sd.data_ptr(), yd.data_ptr(), q.data_ptr(),
+                                s.data_ptr(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+        return [t.clone() for t in (yd, q, s)] + ([] if sd is None else [sd.clone()])
+
+    def fresh():
+        return x.cuda(), r.cuda()
+
+    xd, rd = fresh()
+    alone = call(xd, None, None, torch.empty_like(xd))
+    both = call(xd, rd, torch.empty_like(xd), torch.empty_like(xd))
+    for form in range(3):
+        xd, rd = fresh()
+        want = both if form else alone
+        got = call(xd, None, None, xd) if form == 0 else call(xd, rd, rd, xd) if form == 1 else call(xd, rd, xd, rd)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), form
