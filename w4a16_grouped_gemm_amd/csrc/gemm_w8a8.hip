@@ -868,6 +868,10 @@ struct Load {
 //     768: 5.9 against 7.1)
 //   256 x 256 where it gives nearly every CU a tile (dense 4096 x 4096 x 7168 112 against 132 with
 //     256 x 128 and 159 with 128 x 128)
+// Dense products of 33 to some hundred rows have no form that splits K, and few workgroups: 64, 128
+// and 256 rows of 4096 x 4096 take 22 us each (32, 64 and 128 workgroups), of 2112 x 7168 36 (17,
+// 34 and 68), beside 3.3 and 3.0 us for reading the weights; the border at 32 rows is one between
+// what there is (30 x 4096 x 4096 10.8)
 template <int KIND, bool F32>
 hipError_t launch_kind(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 {

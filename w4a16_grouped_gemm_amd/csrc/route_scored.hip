@@ -20,12 +20,16 @@
 // Lane q of the TL lanes that hold a token has its experts q PL .. q PL + PL - 1
 // (so groups of experts are groups of neighbouring lanes, reduced by DPP); k
 // rounds take the largest remaining key (the order-preserving integer image of
-// c) and retire it. Bound by instructions. With TL = 64 a token costs about 570
-// of them, most in the rounds, whose reductions then serve one token; with TL =
-// 16 four tokens share a wave and its rounds, about 300 each, but the wave takes
-// twice as long. 256 experts in 8 groups, top 8, us with 64 lanes and with 16:
-// 2048 tokens 4.6 and 6.1, 4096 6.5 and 6.2, 8192 10.2 and 8.4, 32768 31.6 and
-// 22.7.
+// c) and retire it. Bound by the rounds' chain, each a maximum over lanes, a
+// ballot and a select that wait for one another: 8192 tokens give two waves per
+// SIMD, and vector instructions are active in 52% of the busy cycles. With TL =
+// 64 a token costs 632 of them, most in the rounds, whose reductions then serve
+// one token; with TL = 16 four tokens share a wave and its rounds, 313 each, but
+// the wave takes twice as long. 256 experts in 8 groups, top 8, us with 64 lanes
+// and with 16: 2048 tokens 4.6 and 6.1, 4096 6.5 and 6.2, 8192 10.2 and 8.6,
+// 32768 31.6 and 22.7. Groups that are not 2^n whole lanes have 64 lanes only, a
+// lane to a group: 160 experts in 8 groups, top 6, 3.9 us for one token, 4.3
+// for 512, 11.0 for 8192.
 #include "route_core.hpp"
 #include "w8a8.hpp"
 
