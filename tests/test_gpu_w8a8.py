@@ -504,3 +504,50 @@ VARIANTS = [  # shapes for the kernel variants that no shape above reaches
 @pytest.mark.parametrize("T,E,begin,L,k,H,I,mode", VARIANTS)
 def test_grouped_in_the_other_variants(T, E, begin, L, k, H, I, mode):
     test_grouped(T, E, begin, L, k, H, I, mode)
+
+
+def test_workspace_of_the_caller_may_hold_anything():
+    """One workspace for calls of several sizes, full of ones' bits or of what the last call left: the same results."""
+    from w4a16_grouped_gemm_amd import ops
+    space = None
+    for T, E, L, begin, k, H, I in [(700, 16, 16, 0, 4, 512, 384), (3, 16, 8, 4, 4, 512, 384), (64, 64, 64, 0, 8, 2048, 768),
+                                    (1, 64, 64, 0, 8, 2048, 768), (300, 16, 4, 12, 2, 256, 256)]:
+        x, ids, w, w13, s13, w2, s2 = layer_inputs(T, E, begin, L, k, H, I, "uniform", T + H)
+        xq, xs = ops.int8_quantize(x)
+        kw = dict(num_experts=E, expert_begin=begin)
+        want = ops.moe_w8a8_forward(xq, xs, ids, w, w13, s13, w2, s2, **kw)
+        if space is None:
+            space = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        for fill in (255, None):
+            if fill is not None:
+                space.fill_(fill)
+            assert torch.equal(ops.moe_w8a8_forward(xq, xs, ids, w, w13, s13, w2, s2, workspace=space, **kw), want)
+
+
+def test_two_threads():
+    """Two threads, each with its stream and its own sizes, through the same binding."""
+    import threading
+    ins = [block_inputs(T, 16, 256, 384, T) for T in (5, 300)]
+    want = [block(*n, 4) for n in ins]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i].append(block(*ins[i], 4))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                                    # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for i in range(2):
+        assert len(got[i]) == 20
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
