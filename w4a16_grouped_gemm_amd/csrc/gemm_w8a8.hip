@@ -113,7 +113,8 @@ __device__ __forceinline__ bool pick_chunk(const W8Args &p, int CS, int e0, int 
         if (at) {
             const int l = __builtin_ctzll(at);
             e = e0 + 64 * i + l;
-            r0 = __builtin_amdgcn_readlane(c.o0[i], l) + (chunk - __builtin_amdgcn_readlane(c.first[i], l)) * CS;
+            r0 = (int)((uint32_t)__builtin_amdgcn_readlane(c.o0[i], l) +
+                       (uint32_t)(chunk - __builtin_amdgcn_readlane(c.first[i], l)) * (uint32_t)CS);
             const int end = min(__builtin_amdgcn_readlane(c.o1[i], l), p.max_rows);
             found = r0 >= 0 && r0 < end;               // compared: a difference could pass 32 bits
             rows = end - r0;
