@@ -8,10 +8,11 @@
 // weight rows as operand A and the tokens as operand B, so that a result lane
 // holds four (four times four) consecutive outputs of one token. Both operands
 // take the same permutation of K, which leaves the sums as they are.
-#include <cmath>
 #include <mutex>
 
+#include "expert_chunks.hpp"
 #include "gemm_core.hpp"
+#include "lds_copy.hpp"
 #include "w8a8.hpp"
 
 namespace moe {
@@ -40,154 +41,6 @@ struct W8Args {
     void *c;
     int K, N;
 };
-
-// Activation row of result row r, in two steps: the index entry (0 where there
-// is no index; loaded first, ahead of what can go out without it), then the row,
-// kept inside the array whatever the entry holds.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t index_rsrc(const W8Args &p)
-{
-    return make_rsrc(p.a_row_index, p.a_row_index ? (uint32_t)p.max_rows * 4u : 0u);
-}
-
-__device__ __forceinline__ int load_index(__amdgpu_buffer_rsrc_t ri, int r)
-{
-    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, (uint32_t)r * 4u, 0, 0);
-}
-
-__device__ __forceinline__ int act_row(const W8Args &p, int r, int i)
-{
-    i = i < 0 ? 0 : (i < p.max_rows ? i : p.max_rows - 1);
-    return p.a_row_index ? i / p.top_k : r;
-}
-
-// The chunks (at most CS rows of one expert each) as one wave sees them, four
-// experts to a lane: expert 64 i + lane has n[i] chunks, the first of them
-// chunk first[i]. All offsets are loaded before the first is used; past 256
-// experts the rest is scanned in rounds of 256. Offsets are the caller's. An
-// expert has at least 0 and at most as many chunks as all rows would give it,
-// so that the numbers stay in 32 bits and in order whatever the offsets hold, and
-// a chunk counts only where its rows are in the arrays (pick_chunk). CLAMP: each
-// offset is moved into the rows first, so that the total counts no other chunks
-// (the tile kernel shares the total out; in the streaming kernel, whose
-// workgroups each look for one chunk, 64 tokens' gate/up took 69.0 us with it
-// and takes 68.2).
-constexpr int kScan = 4;
-
-struct Chunks {
-    int o0[kScan], o1[kScan], first[kScan], n[kScan];
-};
-
-// Experts e0 .. e0 + 255, whose first chunk is `before`; returns the next one's.
-template <bool CLAMP>
-__device__ __forceinline__ int scan_chunks(const W8Args &p, uint32_t CS, int lane, int e0, int before, Chunks &c)
-{
-#pragma unroll
-    for (int i = 0; i < kScan; ++i) {
-        const int e = e0 + 64 * i + lane, ee = e < p.E ? e : p.E - 1;
-        c.o0[i] = p.offsets[ee];
-        c.o1[i] = p.offsets[ee + 1];
-    }
-#pragma unroll
-    for (int i = 0; i < kScan; ++i) {
-        if constexpr (CLAMP) {
-            c.o0[i] = min(max(c.o0[i], 0), p.max_rows);
-            c.o1[i] = min(max(c.o1[i], 0), p.max_rows);
-        }
-        const uint32_t rows = __builtin_elementwise_sub_sat((uint32_t)c.o1[i], (uint32_t)c.o0[i]);
-        c.n[i] = e0 + 64 * i + lane < p.E ? (int)min((rows + CS - 1) / CS, (uint32_t)p.max_rows / CS + 1) : 0;
-        int total;
-        c.first[i] = before + wave_exclusive_scan(c.n[i], total);
-        before += total;
-    }
-    return before;
-}
-
-// Chunk `chunk`, where it is one of c's: its expert, first row and rows.
-__device__ __forceinline__ bool pick_chunk(const W8Args &p, int CS, int e0, int chunk, const Chunks &c, int &e, int &r0,
-                                           int &rows)
-{
-    bool found = false;
-#pragma unroll
-    for (int i = 0; i < kScan; ++i) {
-        const uint64_t at = __ballot(c.first[i] <= chunk && chunk < c.first[i] + c.n[i]);
-        if (at) {
-            const int l = __builtin_ctzll(at);
-            e = e0 + 64 * i + l;
-            r0 = (int)((uint32_t)__builtin_amdgcn_readlane(c.o0[i], l) +
-                       (uint32_t)(chunk - __builtin_amdgcn_readlane(c.first[i], l)) * (uint32_t)CS);
-            const int end = min(__builtin_amdgcn_readlane(c.o1[i], l), p.max_rows);
-            found = r0 >= 0 && r0 < end;               // compared: a difference could pass 32 bits
-            rows = end - r0;
-        }
-    }
-    rows = rows < CS ? rows : CS;
-    return found;
-}
-
-__device__ __forceinline__ bool dense_chunk(const W8Args &p, int CS, int chunk, int &e, int &r0, int &rows)
-{
-    e = 0;
-    r0 = chunk * CS;
-    rows = p.max_rows - r0;
-    rows = rows < CS ? rows : CS;
-    return rows > 0;
-}
-
-// Chunk `chunk`: its expert, first row and rows; false past the last chunk. One
-// wave, every lane gets the result.
-template <bool CLAMP>
-__device__ __forceinline__ bool find_chunk(const W8Args &p, int CS, int chunk, int lane, int &e, int &r0, int &rows)
-{
-    if (!p.offsets)
-        return dense_chunk(p, CS, chunk, e, r0, rows);
-    e = r0 = rows = 0;
-    for (int e0 = 0, before = 0; e0 < p.E; e0 += 64 * kScan) {
-        Chunks c;
-        before = scan_chunks<CLAMP>(p, CS, lane, e0, before, c);
-        if (chunk < before)
-            return pick_chunk(p, CS, e0, chunk, c, e, r0, rows);
-    }
-    return false;
-}
-
-// Tile (chunk of rows, column tile) of linear index i: the column tiles of
-// groups of eight chunks, so that the workgroups running at one time share both
-// operands.
-__device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
-{
-    constexpr int G = 8;
-    const int g = i / (G * tn), rest = i - g * G * tn;
-    const int gm = tm - g * G < G ? tm - g * G : G;
-    m = g * G + rest % gm;
-    n = rest / gm;
-}
-
-// Workgroup b's tile of the tiles that there are (the grid holds as many as
-// there can be): XCD x (workgroups x, x + 8, ...) takes the x-th share of them,
-// so that those which share operands also share an L2. False where b has none.
-__device__ __forceinline__ bool find_tile(const W8Args &p, int CS, int tn, int b, int lane, int &e, int &r0, int &rows,
-                                          int &nt)
-{
-    Chunks c;
-    int tm = 0;
-    if (!p.offsets)
-        tm = (p.max_rows + CS - 1) / CS;
-    else
-        for (int e0 = 0; e0 < p.E; e0 += 64 * kScan)
-            tm = scan_chunks<true>(p, CS, lane, e0, tm, c);
-    const int total = tm * tn, per = total / kXcds, extra = total % kXcds;
-    const int x = b % kXcds, ix = b / kXcds;
-    if (ix >= per + (x < extra ? 1 : 0))
-        return false;
-    int mt;
-    tile_of(x * per + (x < extra ? x : extra) + ix, tm, tn, mt, nt);
-    if (!p.offsets)
-        return dense_chunk(p, CS, mt, e, r0, rows);
-    e = r0 = rows = 0;
-    if (p.E <= 64 * kScan)
-        return pick_chunk(p, CS, 0, mt, c, e, r0, rows);
-    return find_chunk<true>(p, CS, mt, lane, e, r0, rows);
-}
 
 // ---------------------------------------------------------------------------
 // Few rows per expert: the weights are what such a call has to read, once. Each
@@ -426,14 +279,6 @@ __global__ __launch_bounds__(256, 2) void w8_stream_kernel(W8Args p, int blocks)
     }
 }
 
-// At most this many chunks of CS rows: the full ones and one part-filled per expert with rows.
-long long chunks_at_most(const W8GemmLaunch &g, int CS)
-{
-    if (!g.offsets)
-        return (g.max_rows + CS - 1) / CS;
-    return (long long)g.max_rows / CS + (g.num_experts < g.max_rows ? g.num_experts : g.max_rows);
-}
-
 template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING, int QV = 0>
 hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 {
@@ -473,26 +318,6 @@ hipError_t launch_stream(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
 constexpr int kStageK = 64;
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) unsigned char lds_byte;
-
-constexpr uint32_t vmcnt_imm(int n)                   // s_waitcnt vmcnt(n), other counters untouched
-{
-    return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-// 16 bytes per lane from memory to LDS: lane l's to dst + 16 l
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, lds_byte *dst, uint32_t voff, uint32_t soff)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
-}
-
-template <int N>
-__device__ __forceinline__ void wait_for()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(N));
-    __builtin_amdgcn_sched_barrier(0);
-}
 
 // The wait of an early step s < NS - 3, while copies that went out weights first
 // are still on their way: the tokens' of NS - 3 - s stages, and s whole stages.
@@ -504,37 +329,6 @@ __device__ __forceinline__ void early_wait(int s)
             wait_for<(NS - 3 - F) * LM + F * L>();
         else
             early_wait<NS, LM, L, F + 1>(s);
-    }
-}
-
-template <int N>
-__device__ __forceinline__ void wait_barrier()
-{
-    wait_for<N>();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// How many of n things spread evenly over m places come before place i.
-constexpr int spread_to(int i, int n, int m) { return i * n / m; }
-
-// The order of a half step's instructions: its LDS reads and its copies to LDS
-// spread evenly behind the MFMAs, so that none of them holds the matrix unit's
-// next instruction back. (The half step issues them in this order already.)
-template <int MFMAS, int READS, int COPIES>
-__device__ __forceinline__ void spread()
-{
-#pragma unroll
-    for (int i = 0; i < MFMAS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-#pragma unroll
-        for (int j = spread_to(i, READS, MFMAS); j < spread_to(i + 1, READS, MFMAS); ++j)
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-#pragma unroll
-        for (int j = spread_to(i, COPIES, MFMAS); j < spread_to(i + 1, COPIES, MFMAS); ++j)
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
 }
 
@@ -823,27 +617,6 @@ hipError_t launch_tile(const W8GemmLaunch &g, const W8Args &p, hipStream_t st)
                        tn);
     return hipGetLastError();
 }
-
-// The expected rows of an expert that has any, and the tiles that a kernel of BN weight rows x BM tokens would have.
-struct Load {
-    double reached, per;
-    int cols, half;                                     // output columns; 2 where a column has two weight rows
-
-    explicit Load(const W8GemmLaunch &g)
-    {
-        const double R = g.expected_rows < 1 ? 1.0 : (double)g.expected_rows;
-        reached = g.offsets ? g.num_experts * (1.0 - pow(1.0 - 1.0 / g.num_experts, R)) : 1.0;
-        per = R / reached;
-        half = g.kind == MOE_GEMM_W13_SWIGLU ? 2 : 1;
-        cols = g.N / half;
-    }
-
-    double items(int BN, int BM) const
-    {
-        const int BC = BN / half;
-        return reached * ceil(per / BM) * ((cols + BC - 1) / BC);
-    }
-};
 
 // Which kernel, from the expected rows R' of an expert that has any and the
 // tiles (items) that each kernel would have; us on MI355X, operands rotating

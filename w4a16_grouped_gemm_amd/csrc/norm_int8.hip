@@ -18,31 +18,12 @@
 // and had the second half of a row's work wait for the stores of the first (1 x 7168
 // with the residual 5.0 us, now 2.7; 1 x 2048 2.8 and 2.2).
 #include "gemm_core.hpp"
+#include "norm_core.hpp"
 #include "w8a8.hpp"
 
 namespace moe {
 
 namespace {
-
-template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float *s_red)
-{
-    float v = __uint_as_float(wave_reduce(__float_as_uint(x), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    }));
-    if constexpr (TPR > 64) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0)
-            s_red[wave] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < TPR / 64; ++w)
-            v += s_red[w];
-        __syncthreads();
-    }
-    return v;
-}
 
 template <int TPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, float *s_red)
@@ -63,10 +44,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float *s_red)
     }
     return v;
 }
-
-// A mean of squares plus eps from which the norm is not taken: past binary32's range (or NaN), or so small that
-// squares lost bits, or all of them.
-__device__ __forceinline__ bool out_of_range(float ms) { return !(ms >= 0x1p-100f && ms < __builtin_inff()); }
 
 // The norm of a row of finite values out of binary32's range for squares: the squares are those of the row times a
 // power of two f, which keeps any bf16 row's within it. Small rows are taken times f, since their rstd may be too
