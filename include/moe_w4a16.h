@@ -466,6 +466,100 @@ moe_status moe_w8a8_forward(const moe_shape *shape, const int8_t *x, const float
                             const float *w2_s, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * ---- The FP8 variant: e4m3 weights and activations, blocks of 128 ----
+ * A code is an OCP e4m3 byte (largest value 448, no infinities). Activations
+ * have a binary32 scale for each 128 consecutive values of a row, weights one
+ * for each block of 128 rows x 128 columns (the last block of rows may be less):
+ *   a     uint8 [rows][K],   a_scale f32 [rows][K/128]
+ *   w13_q uint8 [E_loc][2*I][H], w13_s f32 [E_loc][2*I/128][H/128]
+ *   w2_q  uint8 [E_loc][H][I],   w2_s  f32 [E_loc][H/128][I/128]
+ * The entry points that take a moe_shape require group_size == 128 and plain
+ * weights (else MOE_ERR_UNSUPPORTED). Products:
+ *   c[r][n] = sum_g (a_scale[r][g] * w_scale[n/128][g]) * sum_{k in g} a[r][k] w[n][k]
+ * groups g of 128 in binary32 with one fused multiply-add each. For binary32
+ * results a group's sum is binary32's; for bf16 results it is the FP8 matrix
+ * instruction's, which aligns the products of a run of eight to the largest and
+ * keeps 13 bits below it.
+ */
+
+/*
+ * Rows of K bf16 values (K a multiple of 128, <= 65536) to FP8. For each block
+ * of 128 values v:
+ *   scale = max|v| / 448, or with pow2 the least power of two that is not less
+ *   q     = e4m3(v / scale), the exact quotient to the nearest code, ties to the
+ *           even one (without pow2: of 448 v / max|v|)
+ * A block whose largest |v| is below 2^-100 gets codes and scale 0; a block with
+ * a NaN or an infinity gets codes 0 and a NaN scale, so that whatever is computed
+ * from it is NaN. q uint8 [rows][K], q_scale f32 [rows][K/128]; the outputs must
+ * not overlap x. Limits of rows as in moe_rms_norm.
+ */
+moe_status moe_fp8_quantize(int64_t rows, int32_t K, const uint16_t *x, int32_t pow2, uint8_t *q, float *q_scale,
+                            void *stream);
+
+/*
+ * RMS norm of rows of K bf16 values with the residual's addition, to FP8:
+ *   h = bf16(x + residual)          (h = x when residual is NULL)
+ *   v = h * weight * rstd,          rstd = 1 / sqrt(mean(h^2) + eps)
+ *   q, q_scale: blocks of v as in moe_fp8_quantize. The quotients v / max|v| are
+ *   those of the exact products h * weight (rstd cancels); with pow2, v is a
+ *   binary32 value.
+ *   sum = h (given with residual, and only then); y = bf16(v) as moe_rms_norm
+ *   gives it (NULL: not wanted)
+ * Arguments, in-place forms, limits of rows and rows out of range as in
+ * moe_rms_norm, K a multiple of 128. A row with a NaN or an infinity, or of zeros
+ * with eps 0, gets NaN scales throughout.
+ */
+moe_status moe_rms_norm_fp8(int64_t rows, int32_t K, const uint16_t *x, const uint16_t *residual, const uint16_t *weight,
+                            float eps, int32_t pow2, uint16_t *sum, uint16_t *y, uint8_t *q, float *q_scale, void *stream);
+
+/*
+ * E weight matrices bf16 [E][N][K] (K a multiple of 128, <= 65536; N <= 262144)
+ * to FP8 codes [E][N][K] with a scale for each block of 128 x 128,
+ * [E][ceil(N/128)][K/128], scale and codes of a block as in moe_fp8_quantize.
+ * Fewer than 2^24 blocks in all (MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_fp8_quantize_weights(int32_t E, int32_t N, int32_t K, const uint16_t *w, int32_t pow2, uint8_t *q,
+                                    float *q_scale, void *stream);
+
+/*
+ * Dense FP8 product, as above.
+ *   M >= 0 (0: no-op); N a multiple of 16, <= 262144; K a multiple of 128,
+ *   <= 65536; N*K and M*K below 2^31, M*N below 2^36 (MOE_ERR_UNSUPPORTED beyond)
+ *   a [M][K], a_scale [M][K/128], wq [N][K], w_scale [ceil(N/128)][K/128],
+ *   c [M][N] bf16 (RNE) or f32 (c_dtype)
+ */
+moe_status moe_fp8_dense_gemm(int32_t M, int32_t N, int32_t K, const uint8_t *a, const float *a_scale, const uint8_t *wq,
+                              const float *w_scale, void *c, moe_dtype c_dtype, void *stream);
+
+/*
+ * Grouped FP8 product over expert slabs, the row semantics of
+ * moe_grouped_gemm_w8a8: for local expert e and rows r in
+ * [offsets[e], offsets[e+1]) the activation row is row a_row_index[r] / top_k
+ * of (a [T][K], a_scale [T][K/128]) when a_row_index != NULL, else row r of
+ * (a [T*k][K], a_scale [T*k][K/128]). Kinds and outputs as there (W13_SWIGLU: bf16
+ * h = silu(g) * u; W2 / W13_RAW: bf16 or f32); rows >= R of c are untouched.
+ * The grid never depends on the counts, no workspace. Whatever offsets and
+ * a_row_index hold, only these arrays' rows are read and written.
+ */
+moe_status moe_grouped_gemm_fp8(const moe_shape *shape, moe_gemm_kind kind, const uint8_t *a, const float *a_scale,
+                                const int32_t *a_row_index, const int32_t *offsets, const uint8_t *wq,
+                                const float *w_scale, void *c, moe_dtype c_dtype, void *stream);
+
+/*
+ * The FP8 layer after routing: permute -> gate/up (h = bf16(silu(g) * u)) -> h to
+ * FP8 (pow2 as in moe_fp8_quantize) -> down (y bf16) -> finalize. Rows x and routing
+ * as in moe_w8a8_forward.
+ *   x uint8 [T][H], x_scale f32 [T][H/128], out bf16 [T][H] (+0.0 for a token with
+ *   no local slot); workspace >= moe_fp8_workspace_size bytes (0 for an invalid
+ *   shape), 256-B aligned, no state between calls.
+ */
+size_t moe_fp8_workspace_size(const moe_shape *shape);
+moe_status moe_fp8_forward(const moe_shape *shape, const uint8_t *x, const float *x_scale, const int32_t *topk_ids,
+                           const float *topk_w, const uint8_t *w13_q, const float *w13_s, const uint8_t *w2_q,
+                           const float *w2_s, int32_t pow2, uint16_t *out, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
  * Top-k routing on scores, for routers that moe_route (softmax of the k chosen
  * logits) does not cover. Per token, with logits l, bias b (NULL: 0):
  *   s = sigmoid(l) or softmax(l) over all E_g, rounded to binary32

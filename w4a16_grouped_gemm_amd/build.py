@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libmoe_w4a16.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "gemm_w4a16.hip", "decode.hip", "gemm_mxfp4.hip", "finalize.hip", "pack.hip",
-           "route_scored.hip", "norm_int8.hip", "gemm_w8a8.hip", "api_w8a8.hip"]
+           "route_scored.hip", "norm_int8.hip", "gemm_w8a8.hip", "api_w8a8.hip", "norm_fp8.hip", "gemm_fp8.hip",
+           "api_fp8.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

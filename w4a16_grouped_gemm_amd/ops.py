@@ -35,7 +35,9 @@ EXPORTED = ["moe_status_str", "moe_w4a16_check_shape", "moe_w4a16_is_supported",
             "moe_w4a16_set_launch_override", "moe_w4a16_forward_noalloc", "moe_mxfp4_quantize",
             "moe_grouped_gemm_mxfp4", "moe_w4a4_workspace_size", "moe_w4a4_forward",
             "moe_mxfp4_pack_weights", "moe_rms_norm", "moe_int8_quantize", "moe_w8a8_dense_gemm",
-            "moe_grouped_gemm_w8a8", "moe_w8a8_workspace_size", "moe_w8a8_forward", "moe_route_scored"]
+            "moe_grouped_gemm_w8a8", "moe_w8a8_workspace_size", "moe_w8a8_forward", "moe_route_scored",
+            "moe_fp8_quantize", "moe_rms_norm_fp8", "moe_fp8_quantize_weights", "moe_fp8_dense_gemm",
+            "moe_grouped_gemm_fp8", "moe_fp8_workspace_size", "moe_fp8_forward"]
 
 
 class MoeShape(ctypes.Structure):
@@ -137,6 +139,20 @@ def load_library(path: str = LIB_PATH):
         lib.moe_w8a8_forward.restype = I
         lib.moe_route_scored.argtypes = [S, ctypes.POINTER(Router), P, P, P, P, P]
         lib.moe_route_scored.restype = I
+        lib.moe_fp8_quantize.argtypes = [ctypes.c_int64, i32, P, i32, P, P, P]
+        lib.moe_fp8_quantize.restype = I
+        lib.moe_rms_norm_fp8.argtypes = [ctypes.c_int64, i32, P, P, P, F, i32, P, P, P, P, P]
+        lib.moe_rms_norm_fp8.restype = I
+        lib.moe_fp8_quantize_weights.argtypes = [i32, i32, i32, P, i32, P, P, P]
+        lib.moe_fp8_quantize_weights.restype = I
+        lib.moe_fp8_dense_gemm.argtypes = [i32, i32, i32, P, P, P, P, P, I, P]
+        lib.moe_fp8_dense_gemm.restype = I
+        lib.moe_grouped_gemm_fp8.argtypes = [S, I, P, P, P, P, P, P, P, I, P]
+        lib.moe_grouped_gemm_fp8.restype = I
+        lib.moe_fp8_workspace_size.argtypes = [S]
+        lib.moe_fp8_workspace_size.restype = Z
+        lib.moe_fp8_forward.argtypes = [S, P, P, P, P, P, P, P, P, i32, P, P, Z, P]
+        lib.moe_fp8_forward.restype = I
         _lib = lib
         return lib
 
@@ -858,4 +874,217 @@ def moe_w8a8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Ten
     _check(lib.moe_w8a8_forward(sh, x.data_ptr(), x_scale.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
                                 w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), out.data_ptr(),
                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current_stream(index)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the FP8 variant: e4m3 codes with a float32 scale for each 128 values of a row
+# (activations) or 128 x 128 values (weights)
+# ---------------------------------------------------------------------------
+
+FP8 = torch.float8_e4m3fn
+
+
+def _block_scales(shape):
+    """A float32 for each 128 values of rows of this shape."""
+    size = (*shape[:-1], shape[-1] // 128)
+    return torch.empty(size, dtype=torch.float32, device="cuda") if len(size) != 2 else _empty(size, (size[1], 1), torch.float32)
+
+
+def fp8_quantize(x: torch.Tensor, *, pow2: bool = False, stream=None):
+    """bf16 rows -> (codes float8_e4m3fn, scales float32 for each 128 values): code * scale stands for the value.
+
+    pow2: scales that are powers of two."""
+    index = _on_gpu(x, "x")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return fp8_quantize(x, pow2=pow2)
+    shape = x.shape
+    K = shape[-1] if shape else 0
+    _expect(x, torch.bfloat16, index, shape, "x")
+    if K % 128 or K == 0:
+        raise MoeError(2, "rows must be multiples of 128 values")
+    q, s = _empty(tuple(shape), x.stride(), FP8), _block_scales(shape)
+    _check((_lib or load_library()).moe_fp8_quantize(x.numel() // K, K, x.data_ptr(), bool(pow2), q.data_ptr(), s.data_ptr(),
+                                                     _current_stream(index)))
+    return q, s
+
+
+def _rms_norm_fp8(x, residual, weight, eps, pow2, sum_out, bf16, stream):
+    index = _on_gpu(x, "x")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return _rms_norm_fp8(x, residual, weight, eps, pow2, sum_out, bf16, None)
+    shape = x.shape
+    K = shape[-1] if shape else 0
+    _expect(x, torch.bfloat16, index, shape, "x")
+    _expect(weight, torch.bfloat16, index, (K,), "weight")
+    if K % 128 or K == 0:
+        raise MoeError(2, "rows must be multiples of 128 values")
+    size, stride = tuple(shape), x.stride()
+    if residual is not None:
+        _expect(residual, torch.bfloat16, index, shape, "residual")
+        if sum_out is None:
+            sum_out = _empty(size, stride, torch.bfloat16)
+        else:
+            _expect(sum_out, torch.bfloat16, index, shape, "sum_out")
+    y = _empty(size, stride, torch.bfloat16) if bf16 else None
+    q, s = _empty(size, stride, FP8), _block_scales(shape)
+    _check((_lib or load_library()).moe_rms_norm_fp8(
+        x.numel() // K, K, x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), eps,
+        bool(pow2), None if residual is None else sum_out.data_ptr(), y.data_ptr() if bf16 else None, q.data_ptr(),
+        s.data_ptr(), _current_stream(index)))
+    return y, q, s, sum_out
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, pow2: bool = False,
+                 with_bf16: bool = False, stream=None):
+    """RMS norm with FP8 rows: (codes float8_e4m3fn, scales float32 for each 128 values[, the bf16 rows])."""
+    y, q, s, _ = _rms_norm_fp8(x, None, weight, eps, pow2, None, with_bf16, stream)
+    return (q, s, y) if with_bf16 else (q, s)
+
+
+def add_rms_norm_fp8(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                     pow2: bool = False, sum_out: torch.Tensor | None = None, with_bf16: bool = False, stream=None):
+    """RMS norm of x + residual with FP8 rows: (codes, scales for each 128 values, x + residual[, the bf16 rows]).
+
+    sum_out may be residual or x itself (in place). with_bf16: a router reads the unquantized rows."""
+    if residual is None:
+        raise ValueError("residual is required")
+    y, q, s, h = _rms_norm_fp8(x, residual, weight, eps, pow2, sum_out, with_bf16, stream)
+    return (q, s, h, y) if with_bf16 else (q, s, h)
+
+
+def fp8_quantize_weights(w: torch.Tensor, *, pow2: bool = False, stream=None):
+    """bf16 weights [N, K] or [E, N, K] -> (codes float8_e4m3fn, scales float32 for each block of 128 x 128,
+    [ceil(N/128), K/128] or with E in front)."""
+    index = _on_gpu(w, "w")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return fp8_quantize_weights(w, pow2=pow2)
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    _expect(w, torch.bfloat16, index, w.shape, "w")
+    N, K = w.shape[-2:]
+    if K % 128 or K == 0:
+        raise MoeError(2, "rows must be multiples of 128 values")
+    q = torch.empty(w.shape, dtype=FP8, device=w.device)
+    s = torch.empty((*w.shape[:-2], (N + 127) // 128, K // 128), dtype=torch.float32, device=w.device)
+    _check((_lib or load_library()).moe_fp8_quantize_weights(w.shape[0] if w.dim() == 3 else 1, N, K, w.data_ptr(),
+                                                             bool(pow2), q.data_ptr(), s.data_ptr(), _current_stream(index)))
+    return q, s
+
+
+def dense_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, *,
+                   out_dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Dense FP8 product c [M, N] of rows a [M, K] (a_scale [M, K/128]) and weights wq [N, K]
+    (w_scale [ceil(N/128), K/128])."""
+    index = _on_gpu(a, "a")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return dense_gemm_fp8(a, a_scale, wq, w_scale, out_dtype=out_dtype, out=out)
+    if a.dim() != 2 or wq.dim() != 2:
+        raise ValueError("a must be [M, K] and wq [N, K]")
+    M, K = a.shape
+    N = wq.shape[0]
+    _expect(a, FP8, index, (M, K), "a")
+    _expect(a_scale, torch.float32, index, (M, K // 128), "a_scale")
+    _expect(wq, FP8, index, (N, K), "wq")
+    _expect(w_scale, torch.float32, index, ((N + 127) // 128, K // 128), "w_scale")
+    if out is None:
+        dt = _out_dtype(out_dtype)
+        out = _empty((M, N), (N, 1), out_dtype)
+    else:
+        dt = _out_dtype(out.dtype)
+        _expect(out, out.dtype, index, (M, N), "out")
+    _check((_lib or load_library()).moe_fp8_dense_gemm(M, N, K, a.data_ptr(), a_scale.data_ptr(), wq.data_ptr(),
+                                                       w_scale.data_ptr(), out.data_ptr(), dt, _current_stream(index)))
+    return out
+
+
+def grouped_gemm_fp8(kind: int, a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor, wq: torch.Tensor,
+                     w_scale: torch.Tensor, *, num_tokens: int, top_k: int, a_row_index: torch.Tensor | None = None,
+                     out_dtype=torch.bfloat16, num_experts: int | None = None, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Grouped FP8 product over expert slabs; returns c [num_tokens*top_k, cols] (rows past the last routed one are
+    not written). kind, offsets and a_row_index as in grouped_gemm_w4a16; wq [E, N, K], w_scale [E, N/128, K/128]."""
+    index = _on_gpu(a, "a")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return grouped_gemm_fp8(kind, a, a_scale, offsets, wq, w_scale, num_tokens=num_tokens, top_k=top_k,
+                                    a_row_index=a_row_index, out_dtype=out_dtype, num_experts=num_experts, out=out)
+    if wq.dim() != 3:
+        raise ValueError("wq must be [E, N, K]")
+    E_loc, N, K = wq.shape
+    if kind != W2 and N % 2:
+        raise ValueError("wq must have a gate row and an up row for each column, an even number")
+    H, I = (N, K) if kind == W2 else (K, N // 2)
+    cols = I if kind == W13_SWIGLU else N
+    num_tokens, top_k = operator.index(num_tokens), operator.index(top_k)
+    rows = num_tokens * top_k
+    a_rows = rows if a_row_index is None else num_tokens
+    _expect(a, FP8, index, (a_rows, K), "a")
+    _expect(a_scale, torch.float32, index, (a_rows, K // 128), "a_scale")
+    _expect(offsets, torch.int32, index, (E_loc + 1,), "offsets")
+    _expect(wq, FP8, index, (E_loc, N, K), "wq")
+    _expect(w_scale, torch.float32, index, (E_loc, N // 128, K // 128), "w_scale")
+    if a_row_index is not None:
+        _expect(a_row_index, torch.int32, index, (rows,), "a_row_index")
+    if out is None:
+        dt = _out_dtype(out_dtype)
+        out = _empty((rows, cols), (cols, 1), out_dtype)
+    else:
+        dt = _out_dtype(out.dtype)
+        _expect(out, out.dtype, index, (rows, cols), "out")
+    _check((_lib or load_library()).moe_grouped_gemm_fp8(
+        _shape_ref(num_tokens, H, I, operator.index(num_experts or E_loc), E_loc, top_k), kind, a.data_ptr(),
+        a_scale.data_ptr(), None if a_row_index is None else a_row_index.data_ptr(), offsets.data_ptr(), wq.data_ptr(),
+        w_scale.data_ptr(), out.data_ptr(), dt, _current_stream(index)))
+    return out
+
+
+def moe_fp8_forward(x: torch.Tensor, x_scale: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                    w13_q: torch.Tensor, w13_s: torch.Tensor, w2_q: torch.Tensor, w2_s: torch.Tensor,
+                    out: torch.Tensor | None = None, stream=None, *, num_experts: int | None = None,
+                    expert_begin: int = 0, pow2: bool = False, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The FP8 expert layer after routing: x float8_e4m3fn [T, H] with x_scale [T, H/128] (add_rms_norm_fp8,
+    fp8_quantize), topk_ids / topk_w from route or route_scored, weights [E_loc, 2I, H] / [E_loc, H, I] with a float32
+    scale for each block of 128 x 128. pow2: the experts' rows between the two products get scales that are powers of
+    two. num_experts: the router's (default: all local). Returns out bf16 [T, H]."""
+    index = _on_gpu(x, "x")
+    if (there := _elsewhere(index, stream)) is not None:
+        with there:
+            return moe_fp8_forward(x, x_scale, topk_ids, topk_w, w13_q, w13_s, w2_q, w2_s, out, num_experts=num_experts,
+                                   expert_begin=expert_begin, pow2=pow2, workspace=workspace)
+    if x.dim() != 2 or topk_ids.dim() != 2 or w13_q.dim() != 3:
+        raise ValueError("x must be [T, H], topk_ids [T, k] and w13_q [E, 2I, H]")
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E_loc, N13, _ = w13_q.shape
+    I = N13 // 2
+    _expect(x, FP8, index, (T, H), "x")
+    _expect(x_scale, torch.float32, index, (T, H // 128), "x_scale")
+    _expect(topk_ids, torch.int32, index, (T, k), "topk_ids")
+    _expect(topk_w, torch.float32, index, (T, k), "topk_w")
+    _expect(w13_q, FP8, index, (E_loc, 2 * I, H), "w13_q")
+    _expect(w13_s, torch.float32, index, (E_loc, 2 * I // 128, H // 128), "w13_s")
+    _expect(w2_q, FP8, index, (E_loc, H, I), "w2_q")
+    _expect(w2_s, torch.float32, index, (E_loc, H // 128, I // 128), "w2_s")
+    if out is None:
+        out = _empty((T, H), (H, 1), torch.bfloat16)
+    else:
+        _expect(out, torch.bfloat16, index, (T, H), "out")
+    lib = _lib or load_library()
+    begin = operator.index(expert_begin)
+    sh = _shape_ref(T, H, I, operator.index(num_experts or begin + E_loc), E_loc, k, begin)
+    if workspace is None:
+        # from the caching allocator at every call: it belongs to this stream, or to the graph that is being captured,
+        # so no two calls that can overlap share one
+        workspace = _empty((max(lib.moe_fp8_workspace_size(sh), 256),), (1,), torch.uint8)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    _check(lib.moe_fp8_forward(sh, x.data_ptr(), x_scale.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
+                               w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), bool(pow2),
+                               out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _current_stream(index)))
     return out
