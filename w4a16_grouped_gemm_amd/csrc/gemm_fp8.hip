@@ -14,6 +14,8 @@
 // group's sum of normal values is off by 1.5e-5 of itself). bf16 results round at
 // 2^-9, far above; binary32 results take the codes through v_mfma_f32_16x16x32_bf16
 // instead, whose sums are binary32's.
+#include <mutex>
+
 #include "expert_chunks.hpp"
 #include "fp8.hpp"
 #include "gemm_core.hpp"
@@ -109,6 +111,9 @@ __device__ __forceinline__ void add_scaled(floatx4 &tot, float s, floatx4 c)
     for (int i = 0; i < 4; ++i)
         tot[i] = __builtin_fmaf(s, c[i], tot[i]);
 }
+
+// v is in vector registers here, as if it were read.
+__device__ __forceinline__ void keep(floatx4 v) { asm volatile("" ::"v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3])); }
 
 __device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
 {
@@ -306,13 +311,645 @@ hipError_t launch_stream(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t s
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Few rows and few workgroups (dense products, a token's experts): the stream
+// through LDS. Each wave streams its own weight rows, TPW tiles of 16, and its chunk's NSUB subtiles
+// of 16 tokens through a part of LDS that no other wave sees, D groups of K ahead:
+// copies straight from memory, eight lanes to a row's 128 bytes, waited for by
+// count, and no meeting of the waves. WK waves of a workgroup share a set of weight
+// rows, each with its part of K, and add their sums in the waves' order in the end.
+//
+// Loads to the registers of the lanes that multiply them take 16 bytes of a row
+// each and pass the cache one lane at a time: 16 x 14336 x 4096 17.1 us in the
+// streaming kernel and 14.0 here, 64 x 4096 x 4096 12.1 and 8.7. Where there are more
+// workgroups than the GPU holds at a time, LDS lets too few of them start early: 128
+// experts of 768 -> 2048 with a row each 26.8 us there, 31 here.
+// ---------------------------------------------------------------------------
+// Copies and loads of a wave that went out behind those of a quad's group j when its turn comes: the groups after it,
+// and the next quads' scales in between.
+constexpr int stream_behind(int D, int j, int copies, int scales)
+{
+    return (D - 1) * copies + (D == 4 || j == 1 || j == 2 ? scales : 0);
+}
+
+template <int KIND, bool F32, int NSUB, int TPW, int WK, int D>
+__global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(Fp8Args p, int blocks)
+{
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    constexpr int TG = SW ? TPW / 2 : TPW;              // tiles side by side: a lane's outputs are 4 TG consecutive ones
+    constexpr int WN = 4 / WK, H = SW ? 2 : 1;
+    constexpr int C = 2 * (TPW + NSUB), kScales = NSUB + H;   // copies of a group, loads of a quad's scales
+    constexpr int kSlot = C * 1024, kWave = D * kSlot;
+    static_assert(D == 2 || D == 4, "groups of a quad");
+    extern __shared__ __align__(16) unsigned char s_dyn[];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int m = lane & 15, q = lane >> 4;
+    const int wn = wave / WK, wk = wave % WK;
+    const int chunk = blockIdx.x / blocks;
+    const int block = blockIdx.x - chunk * blocks;
+    int e, r0, rows;
+    if (!find_chunk<false>(p, 16 * NSUB, chunk, lane, e, r0, rows))
+        return;
+    e = uniform(e);
+    const int cols = SW ? p.N / 2 : p.N;                // outputs per row
+    const int n0 = (block * WN + wn) * 16 * TG;
+    if (WK == 1 && n0 >= cols)
+        return;
+    const int G = p.K / 128;
+    const __amdgpu_buffer_rsrc_t ri = index_rsrc(p), rxs = make_rsrc(p.as, p.a_bytes / 32), rws = scale_rsrc(p, e);
+    const uint8_t *wbase = p.wq + (size_t)e * p.N * p.K;
+    // rows whose chunk this lane copies, 8 rows to a copy; place l of a row's eight 16-byte chunks holds chunk l ^ (row / 2)
+    const uint32_t place = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;
+    int row[2 * NSUB], idx[2 * NSUB], srow[NSUB], sidx[NSUB];
+#pragma unroll
+    for (int j = 0; j < 2 * NSUB; ++j) {
+        const int r = 8 * j + (lane >> 3);
+        row[j] = r0 + (r < rows ? r : rows - 1);
+        idx[j] = load_index(ri, row[j]);
+    }
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s) {
+        srow[s] = r0 + (16 * s + m < rows ? 16 * s + m : rows - 1);
+        sidx[s] = load_index(ri, srow[s]);
+    }
+    // weight row of lane row m in tile t: outputs n0 + (m / 4) 4 TG + 4 t + m % 4 (gate), the same + N / 2 (up)
+    uint32_t wo[2 * TPW], xo[2 * NSUB], so[NSUB];
+#pragma unroll
+    for (int j = 0; j < 2 * TPW; ++j) {
+        const int t = j / 2, r = (j & 1) * 8 + (lane >> 3);
+        int n = n0 + (r >> 2) * 4 * TG + (t % TG) * 4 + (r & 3);
+        n = n < cols ? n : cols - 1;
+        wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * p.K + (place ^ (uint32_t)(j & 1) * 64);
+    }
+    // 16 TG columns from a multiple of 16 TG on are all of one block of 128
+    const uint32_t ws0 = (uint32_t)(n0 < cols ? n0 : cols - 1) / 128 * G * 4, ws1 = ws0 + (uint32_t)(cols / 128) * G * 4;
+    // groups [g, end) are this wave's; those past them are copied from arrays of no bytes, to keep the count
+    int g = wk * G / WK;
+    const int end = (wk + 1) * G / WK;
+    lds_byte *lds = (lds_byte *)s_dyn + wave * kWave;
+    auto copy_w = [&](int k, int slot) {
+        const __amdgpu_buffer_rsrc_t rw = make_rsrc(wbase, k < end ? (uint32_t)p.N * p.K : 0u);
+#pragma unroll
+        for (int j = 0; j < 2 * TPW; ++j)
+            copy16(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
+    };
+    auto copy_x = [&](int k, int slot) {
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, k < end ? p.a_bytes : 0u);
+#pragma unroll
+        for (int j = 0; j < 2 * NSUB; ++j)
+            copy16(rx, lds + slot * kSlot + (2 * TPW + j) * 1024, xo[j], k < end ? k * 128 : 0);
+    };
+    struct Scales {                                     // of four groups
+        floatx4 x[NSUB], w[H];
+    };
+    auto load_scales = [&](Scales &s, int k) {
+#pragma unroll
+        for (int i = 0; i < NSUB; ++i)
+            s.x[i] = __builtin_bit_cast(floatx4, bload16(rxs, so[i] + k * 4, 0));
+        s.w[0] = __builtin_bit_cast(floatx4, bload16(rws, ws0 + k * 4, 0));
+        if constexpr (SW)
+            s.w[1] = __builtin_bit_cast(floatx4, bload16(rws, ws1 + k * 4, 0));
+    };
+    // the first weights set out before the tokens' rows are known
+    copy_w(g, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 2 * NSUB; ++j)
+        xo[j] = (uint32_t)act_row(p, row[j], idx[j]) * p.K + (place ^ (uint32_t)(j & 1) * 64);
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s)
+        so[s] = (uint32_t)act_row(p, srow[s], sidx[s]) * G * 4;
+    Scales sc, sn, sl;                                  // the quad's, the next one's, those under way
+    load_scales(sc, g);
+    if constexpr (D == 2)
+        load_scales(sn, g + 4);
+    __builtin_amdgcn_sched_barrier(0);
+    copy_x(g, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (D == 4)
+        load_scales(sn, g + 4);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 1; j < D; ++j) {
+        copy_w(g + j, j);
+        copy_x(g + j, j);
+    }
+    floatx4 acc[NSUB][TPW];
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s)
+#pragma unroll
+        for (int t = 0; t < TPW; ++t)
+            acc[s][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+    // fragment reads: lane l holds chunks l / 16 and l / 16 + 4 of row l % 16
+    const uint32_t f0 = (uint32_t)(wave * kWave + m * 128 + ((q ^ (m >> 1)) & 7) * 16);
+    auto fragment = [&](int slot, int i) {
+        Frag f;
+        f.lo = *reinterpret_cast<const u32x4 *>(s_dyn + f0 + slot * kSlot + i * 2048);
+        f.hi = *reinterpret_cast<const u32x4 *>(s_dyn + (f0 ^ 64u) + slot * kSlot + i * 2048);
+        return f;
+    };
+    auto turn = [&](auto turn_of) {
+        constexpr int J = decltype(turn_of)::value, SLOT = J % D;
+        wait_for<stream_behind(D, J, C, kScales)>();
+        if (g + J < end) {
+            Frag w[TPW];
+#pragma unroll
+            for (int t = 0; t < TPW; ++t)
+                w[t] = fragment(SLOT, t);
+#pragma unroll
+            for (int s = 0; s < NSUB; ++s) {
+                const Operand<F32> xv(fragment(SLOT, TPW + s));
+#pragma unroll
+                for (int t = 0; t < TPW; ++t) {
+                    add_scaled(acc[s][t], sc.x[s][J] * sc.w[SW && t >= TG ? 1 : 0][J], group_sum(Operand<F32>(w[t]), xv));
+                    keep(acc[s][t]);
+                }
+            }
+        }
+        // every fragment has left LDS
+        __builtin_amdgcn_sched_barrier(0);
+        copy_w(g + J + D, SLOT);
+        copy_x(g + J + D, SLOT);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    for (; g < end; g += 4) {
+        turn(std::integral_constant<int, 0>());
+        load_scales(sl, g + 8);
+        __builtin_amdgcn_sched_barrier(0);
+        turn(std::integral_constant<int, 1>());
+        turn(std::integral_constant<int, 2>());
+        turn(std::integral_constant<int, 3>());
+        sc = sn;
+        sn = sl;
+    }
+    wait_for<0>();                                      // copies past the last group write to LDS too
+    if constexpr (WK > 1) {
+        floatx4 *part = reinterpret_cast<floatx4 *>(s_dyn);   // [WN][WK - 1][NSUB TPW][64]
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < NSUB; ++s)
+#pragma unroll
+            for (int t = 0; t < TPW; ++t)
+                if (wk > 0)
+                    part[((wn * (WK - 1) + wk - 1) * NSUB * TPW + s * TPW + t) * 64 + lane] = acc[s][t];
+        __syncthreads();
+        if (wk > 0)
+            return;
+#pragma unroll
+        for (int i = 0; i < WK - 1; ++i)
+#pragma unroll
+            for (int s = 0; s < NSUB; ++s)
+#pragma unroll
+                for (int t = 0; t < TPW; ++t)
+                    acc[s][t] += part[((wn * (WK - 1) + i) * NSUB * TPW + s * TPW + t) * 64 + lane];
+    }
+    const int nq = n0 + q * 4 * TG;
+#pragma unroll
+    for (int s = 0; s < NSUB; ++s) {
+        if (16 * s + m >= rows)
+            continue;
+        const size_t crow = (size_t)(r0 + 16 * s + m) * cols;
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+            const int n = nq + 4 * t;
+            if (n >= cols)
+                continue;
+            floatx4 v = acc[s][t];
+            if constexpr (SW)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = silu_fast(v[i]) * acc[s][t + TG][i];
+            if constexpr (F32)
+                *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + crow + n) = v;
+            else
+                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + crow + n) =
+                    u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        }
+    }
+}
+
+// A kernel's LDS limit is raised once on each device that launches it.
+template <class Kernel, Kernel *kernel, int BYTES>
+void allow_lds()
+{
+    constexpr int kMaxDevices = 64;
+    static std::once_flag once[kMaxDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
+        return;
+    std::call_once(once[dev], [] {
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    });
+}
+
+template <int KIND, bool F32, int NSUB, int TPW, int WK, int D>
+hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
+{
+    constexpr int TG = KIND == MOE_GEMM_W13_SWIGLU ? TPW / 2 : TPW;
+    const int cols = KIND == MOE_GEMM_W13_SWIGLU ? g.N / 2 : g.N;
+    constexpr int BC = 16 * TG * (4 / WK), kBytes = 4 * D * 2 * (TPW + NSUB) * 1024;
+    static_assert(kBytes >= 4 * NSUB * TPW * 1024, "the waves' sums fit");
+    const int blocks = (cols + BC - 1) / BC;
+    allow_lds<decltype(fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D>), fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D>, kBytes>();
+    hipLaunchKernelGGL((fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D>),
+                       dim3((unsigned)(chunks_at_most(g, 16 * NSUB) * blocks)), dim3(256), kBytes, st, p, blocks);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Many rows per expert: a workgroup of 4 NWM waves computes 64 TN weight rows x
+// 16 TM NWM tokens, a wave 16 TN rows x 16 TM tokens. Both pass through LDS, a
+// group of K (128 bytes) to a stage: the tokens' fragments are read as they are
+// needed, NS stages deep, the weights' a stage ahead into registers, which leaves
+// their place to the group after next. The tokens' scales follow 16 bytes (four
+// groups) at a time, the weights' are all loaded at the start.
+//
+// A stage's rows are 128 bytes, eight 16-byte chunks each; row r keeps chunk c at
+// place c ^ ((r >> 1) & 7), so that the 64 lanes of a fragment read (16 rows x 4
+// chunks) meet no bank conflict. The copies go from memory straight to LDS, 16
+// bytes a lane, eight lanes to a row's 128 bytes: weights loaded by the lanes
+// that multiply them, each from a row of its own, came at 16 bytes a cycle and CU
+// (8192 x 14336 x 4096 495 us with that, 470 so).
+//
+// A group's sums come out of the matrix unit kDelay instructions before their
+// multiply-adds onto the totals, which so run beside the next products.
+// ---------------------------------------------------------------------------
+constexpr int kDelay = 3;                             // MFMAs between a group's sum and its use
+constexpr int kMaxGroups = kMaxNormDim / kGroup;
+
+template <int TN, int TM, int NWM, int NS, int NW>
+struct TileLds {                                      // where things are, in bytes
+    static constexpr int kStage = 16 * TM * NWM * 128, kWeights = 64 * TN * 128;
+    static constexpr int kW = NS * kStage, kScale = kW + NW * kWeights;
+    static constexpr int kScaleCopies = (16 * TM * NWM + 63) / 64;       // 1 KiB each: 64 tokens' scales of four groups
+    static constexpr int kWs = kScale + 2 * kScaleCopies * 1024, kBytes = kWs + 2 * kMaxGroups * 4 + 16;
+};
+
+template <int KIND, bool F32, int TN, int TM, int NWM, int NS, int NW>
+__global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8Args p, int tn)
+{
+    using S = TileLds<TN, TM, NWM, NS, NW>;
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    constexpr int TG = SW ? TN / 2 : TN, H = SW ? 2 : 1;
+    constexpr int BM = 16 * TM * NWM, BC = 64 * TG, kThreads = 256 * NWM;   // tokens, output columns
+    constexpr int L = TM / 2, LW = 2 * TN / NWM;        // copies (loads) of a wave per stage: tokens, weights
+    constexpr int XR = TM % 8 == 0 ? 4 : TM % 6 == 0 ? 3 : 2;   // token fragments in registers
+    constexpr int M = TN * TM / 2;                      // MFMAs of half a stage
+    static_assert(TM % XR == 0 && M % (kDelay + 1) == 0 && TN * XR > kDelay, "rings");
+    static_assert(XR - 1 <= TM / 2, "the next stage's fragments are read in a stage's second half only");
+    static_assert(NS >= 3 && NS <= 5, "the first stages' scales are one copy");
+    extern __shared__ __align__(16) unsigned char s_dyn[];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int wn = wave / NWM, wm = wave % NWM;
+    const int m = lane & 15, q = lane >> 4;
+    int e, r0, rows, nt;
+    if (!find_tile(p, BM, tn, blockIdx.x, lane, e, r0, rows, nt))
+        return;
+    e = uniform(e);
+    r0 = uniform(r0);
+    rows = uniform(rows);
+    const int cols = SW ? p.N / 2 : p.N;
+    const int n0 = nt * BC, nw = n0 + wn * 16 * TG;     // the workgroup's and the wave's first column
+    const uint32_t K = (uint32_t)p.K;
+    const int G = p.K / 128;
+
+    const __amdgpu_buffer_rsrc_t ri = index_rsrc(p);
+    const uint8_t *wbase = p.wq + (size_t)e * p.N * K;
+    lds_byte *lds = (lds_byte *)s_dyn;
+    // rows that this lane copies, a chunk of each, and the row whose scales it copies
+    int xrow[L], xidx[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const int row = (wave * L + j) * 8 + (lane >> 3);
+        xrow[j] = r0 + (row < rows ? row : rows - 1);
+        xidx[j] = load_index(ri, xrow[j]);
+    }
+    int srow = wave * 64 + lane;
+    srow = r0 + (srow < rows ? srow : rows - 1);
+    const int sidx = load_index(ri, srow);
+    // the weights' scales of all groups: the (up to) two blocks of 128 rows that the workgroup's columns are in
+    float *s_ws = reinterpret_cast<float *>(s_dyn + S::kWs);
+    constexpr int kWsLoads = 2 * kMaxGroups / kThreads;
+    float wsr[kWsLoads];
+    {
+        const __amdgpu_buffer_rsrc_t rws = scale_rsrc(p, e);
+        const int last = (cols - 1) / 128;
+        const int b0 = n0 / 128, b1 = SW ? b0 + cols / 128 : (b0 + 1 < last ? b0 + 1 : last);
+#pragma unroll
+        for (int i = 0; i < kWsLoads; ++i) {
+            const int at = threadIdx.x + kThreads * i, h = at >= G ? 1 : 0;
+            wsr[i] = load_f32(rws, at < 2 * G ? (uint32_t)((h ? b1 : b0) * G + at - h * G) * 4 : kOutOfRange, 0);
+        }
+    }
+    const int wsb = SW ? 0 : (nw < cols ? nw / 128 - n0 / 128 : 0) * kMaxGroups;
+    // the weights set out before the tokens' rows are known: row m of tile t is output (m / 4) 4 TG + 4 t + m % 4
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;   // of this lane's row in copies of rows 0 .. 7 of 16
+    uint32_t wo[LW];
+#pragma unroll
+    for (int j = 0; j < LW; ++j) {
+        const int i = wm * LW + j, t = i / 2, r = (i & 1) * 8 + (lane >> 3);
+        int n = nw + (r >> 2) * 4 * TG + (t % TG) * 4 + (r & 3);
+        n = n < cols ? n : cols - 1;
+        wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + (chunk ^ (uint32_t)(i & 1) * 64);
+    }
+    // one of the wave's copies of group g's weights to place `at` (past the last group of nothing, from an array of no bytes)
+    auto copy_w = [&](int j, int g, uint32_t at) {
+        copy16(make_rsrc(wbase, g < G ? (uint32_t)p.N * K : 0u), lds + S::kW + at + wn * (2048 * TN) + (wm * LW + j) * 1024,
+               wo[j], g < G ? g * 128 : 0);
+    };
+#pragma unroll
+    for (int j = 0; j < LW; ++j)
+        copy_w(j, 0, 0);
+    uint32_t xo[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+        xo[j] = (uint32_t)act_row(p, xrow[j], xidx[j]) * K + (chunk ^ (uint32_t)((wave * L + j) & 1) * 64);
+    const uint32_t so = (uint32_t)act_row(p, srow, sidx) * G * 4;
+    const __amdgpu_buffer_rsrc_t rxs = make_rsrc(p.as, p.a_bytes / 32);
+    auto copy_scales = [&](int g) {                     // groups g .. g + 3; for other g, and by other waves, nothing
+        if ((g & 3) == 0 && g < G && wave < S::kScaleCopies)
+            copy16(rxs, lds + S::kScale + ((g >> 2) & 1) * (S::kScaleCopies * 1024) + wave * 1024, so + g * 4, 0);
+    };
+    // one of the L copies of stage g's tokens to place `at`
+    auto copy_x = [&](int j, int g, uint32_t at) {
+        copy16(make_rsrc(p.a, g < G ? p.a_bytes : 0u), lds + at + (wave * L + j) * 1024, xo[j], g < G ? g * 128 : 0);
+    };
+    copy_scales(0);
+#pragma unroll
+    for (int g = 0; g < (NW > NS - 1 ? NW : NS - 1); ++g) {
+#pragma unroll
+        for (int j = 0; j < LW && g > 0 && g < NW; ++j)
+            copy_w(j, g, g * S::kWeights);
+#pragma unroll
+        for (int j = 0; j < L && g < NS - 1; ++j)
+            copy_x(j, g, g * S::kStage);
+    }
+#pragma unroll
+    for (int i = 0; i < kWsLoads; ++i) {
+        const int at = threadIdx.x + kThreads * i, h = at >= G ? 1 : 0;
+        if (at < 2 * G)
+            s_ws[h * kMaxGroups + at - h * G] = wsr[i];
+    }
+
+    // fragment reads: lane l holds chunks l / 16 and l / 16 + 4 of row l % 16
+    const uint32_t f0 = (uint32_t)(m * 128 + ((q ^ (m >> 1)) & 7) * 16);
+    const uint32_t f1 = f0 ^ 64u;
+    const uint32_t x0 = wm * TM * 2048 + f0, x1 = wm * TM * 2048 + f1, xs0 = S::kScale + (wm * TM * 16 + m) * 16;
+    Frag x[XR];
+    float xs[XR], sc[XR][H];
+    Frag w[2][TN];
+    // one of the 2 TN reads of group g's weight fragments
+    auto read_w = [&](Frag (&f)[TN], int j, uint32_t at) {
+        const unsigned char *src = s_dyn + S::kW + at + wn * (2048 * TN) + j / 2 * 2048;
+        if (j & 1)
+            f[j / 2].hi = *reinterpret_cast<const u32x4 *>(src + f1);
+        else
+            f[j / 2].lo = *reinterpret_cast<const u32x4 *>(src + f0);
+    };
+    // one of the three reads of token fragment b: its two chunks, its scales
+    auto read_x = [&](int j, int b, uint32_t at, uint32_t scale_at) {
+        if (j == 0)
+            x[b % XR].lo = *reinterpret_cast<const u32x4 *>(s_dyn + at + x0 + b * 2048);
+        else if (j == 1)
+            x[b % XR].hi = *reinterpret_cast<const u32x4 *>(s_dyn + at + x1 + b * 2048);
+        else
+            xs[b % XR] = *reinterpret_cast<const float *>(s_dyn + scale_at + xs0 + b * 256);
+    };
+    floatx4 tot[TN][TM], c[kDelay + 1];
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+        for (int b = 0; b < TM; ++b)
+            tot[a][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i <= kDelay; ++i)
+        c[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < XR; ++b)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            sc[b][h] = 0.f;
+    auto add = [&](int i) {                             // product i of a stage onto its total, here and not where that is used
+        const int a = i % TN, b = i / TN;
+        add_scaled(tot[a][b], sc[b % XR][SW && a >= TG ? 1 : 0], c[i % (kDelay + 1)]);
+        keep(tot[a][b]);
+    };
+    float wsv[H];
+    uint32_t cur = 0, wcur = 0;                         // places of stage g
+    auto next_place = [&](uint32_t at) { return at == (NS - 1) * S::kStage ? 0u : at + S::kStage; };
+    auto scale_place = [&](int g) { return (uint32_t)(((g >> 2) & 1) * (S::kScaleCopies * 1024) + (g & 3) * 4); };
+    // Half a stage: products of token fragments [HALF TM / 2, ...), XR - 1 fragments read ahead (those of stage g + 1,
+    // at `nxt`, behind the last). Between two products stand the multiply-adds of an earlier one and what there is to
+    // read or to copy, in this order: the compiler's own is full of waits.
+    auto half_stage = [&](auto half, const Frag (&f)[TN], int g, uint32_t nxt, auto copy, auto copies, auto read, auto reads) {
+        constexpr int HALF = decltype(half)::value, COPIES = decltype(copies)::value, READS = decltype(reads)::value;
+#pragma unroll
+        for (int k = 0; k < TM / 2; ++k) {
+            const int b = HALF * TM / 2 + k, ahead = b + XR - 1;
+            const Operand<F32> xv(x[b % XR]);
+#pragma unroll
+            for (int a = 0; a < TN; ++a) {
+                const int i = b * TN + a, at = k * TN + a;
+                c[i % (kDelay + 1)] = group_sum(Operand<F32>(f[a]), xv);
+#pragma unroll
+                for (int j = spread_to(a, 3, TN); j < spread_to(a + 1, 3, TN); ++j)
+                    read_x(j, ahead % TM, ahead < TM ? cur : nxt, scale_place(ahead < TM ? g : g + 1));
+#pragma unroll
+                for (int j = spread_to(at, READS, M); j < spread_to(at + 1, READS, M); ++j)
+                    read(j);
+#pragma unroll
+                for (int j = spread_to(at, COPIES, M); j < spread_to(at + 1, COPIES, M); ++j)
+                    copy(j);
+                add((i + TN * TM - kDelay) % (TN * TM));
+                if (a == 0) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        sc[b % XR][h] = xs[b % XR] * wsv[h];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    // Stage g. In its middle the wave waits for its copies of stage g + 1 and meets the other waves: then stage g + 1 and
+    // its weights are whole, every wave has read all of stage g - 1, whose place takes stage g + NS - 1, and has the
+    // weights of stage g in registers, whose place takes those of stage g + NW. Of the copies under way at the meeting,
+    // those that went out behind stage g + 1's stay so: with two places for weights, which then go before the tokens,
+    // the tokens of NS - 3 stages; with three, which go behind them, the last weights.
+    using Half0 = std::integral_constant<int, 0>;
+    using Half1 = std::integral_constant<int, 1>;
+    using None = std::integral_constant<int, 0>;
+    static_assert(NW == 2 || (NW == 3 && NS == 3), "what stays under way");
+    constexpr bool kWFirst = NW == 2;
+    constexpr int kStay = kWFirst ? (NS - 3) * L : LW;
+    auto stage = [&](const Frag (&f)[TN], Frag (&fn)[TN], int g) {
+        const uint32_t nxt = next_place(cur), wnxt = wcur == (NW - 1) * S::kWeights ? 0u : wcur + S::kWeights;
+        half_stage(Half0(), f, g, nxt, [](int) {}, None(), [](int) {}, None());
+        wait_barrier<kStay>();
+        copy_scales(g + NS - 1);
+        const uint32_t to = cur >= S::kStage ? cur - S::kStage : (NS - 1) * S::kStage;
+        float wsn[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            wsn[h] = s_ws[wsb + h * kMaxGroups + g + 1];
+        half_stage(Half1(), f, g, nxt,
+                   [&](int j) {
+                       if (kWFirst ? j < LW : j >= L)
+                           copy_w(j - (kWFirst ? 0 : L), g + NW, wcur);
+                       else
+                           copy_x(j - (kWFirst ? LW : 0), g + NS - 1, to);
+                   },
+                   std::integral_constant<int, LW + L>(), [&](int j) { read_w(fn, j, wnxt); },
+                   std::integral_constant<int, 2 * TN>());
+        cur = nxt;
+        wcur = wnxt;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            wsv[h] = wsn[h];
+    };
+    // stage 0's tokens and weights are there; behind them went out the rest
+    constexpr int kBehind = (NS - 2) * L + (NW - 1) * LW;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(kBehind) & ~(15u << 8));   // and the weights' scales written to LDS
+    wait_barrier<kBehind>();
+#pragma unroll
+    for (int j = 0; j < 2 * TN; ++j)
+        read_w(w[0], j, 0);
+#pragma unroll
+    for (int b = 0; b < XR - 1; ++b)
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            read_x(j, b, 0, 0);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+        wsv[h] = s_ws[wsb + h * kMaxGroups];
+    // stages in pairs, an odd one first: one way out of the loop, else the compiler holds the totals twice
+    int g = 0;
+    if (G & 1) {
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+            w[1][t] = w[0][t];
+        stage(w[1], w[0], g++);
+    }
+    for (; g < G; g += 2) {
+        stage(w[0], w[1], g);
+        stage(w[1], w[0], g + 1);
+    }
+    wait_for<0>();                                      // the copies past K, which write to LDS, end before the wave does
+#pragma unroll
+    for (int i = TN * TM - kDelay; i < TN * TM; ++i)
+        add(i);
+
+    // a lane's 4 TG outputs of a token are consecutive, four lanes make a run of 16 TG
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int t = (wm * TM + b) * 16 + m, n = nw + q * 4 * TG;
+        if (t >= rows || n >= cols)
+            continue;
+        const size_t at = (size_t)(r0 + t) * cols + n;
+        float v[4 * TG];
+#pragma unroll
+        for (int a = 0; a < TG; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[4 * a + i] = tot[a][b][i];
+                if constexpr (SW)
+                    v[4 * a + i] = silu_fast(v[4 * a + i]) * tot[a + TG][b][i];
+            }
+        // N is a multiple of 16: where the first of a lane's 4 TG <= 16 outputs exists, all do
+#pragma unroll
+        for (int a = 0; a < 4 * TG; a += F32 ? 4 : 8) {
+            if constexpr (F32)
+                *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + at + a) = floatx4{v[a], v[a + 1], v[a + 2], v[a + 3]};
+            else if constexpr (4 * TG >= 8)
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + at + a) =
+                    u32x4{bf16_pair(v[a], v[a + 1]), bf16_pair(v[a + 2], v[a + 3]), bf16_pair(v[a + 4], v[a + 5]),
+                          bf16_pair(v[a + 6], v[a + 7])};
+            else
+                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + at + a) =
+                    u32x2{bf16_pair(v[a], v[a + 1]), bf16_pair(v[a + 2], v[a + 3])};
+        }
+    }
+}
+
+template <int KIND, bool F32, int TN, int TM, int NWM, int NS, int NW>
+hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
+{
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    constexpr int BM = 16 * TM * NWM, BC = 64 * (SW ? TN / 2 : TN);
+    const int cols = SW ? g.N / 2 : g.N;
+    const int tn = (cols + BC - 1) / BC;
+    allow_lds<decltype(fp8_tile_kernel<KIND, F32, TN, TM, NWM, NS, NW>), fp8_tile_kernel<KIND, F32, TN, TM, NWM, NS, NW>,
+              TileLds<TN, TM, NWM, NS, NW>::kBytes>();
+    hipLaunchKernelGGL((fp8_tile_kernel<KIND, F32, TN, TM, NWM, NS, NW>), dim3((unsigned)(chunks_at_most(g, BM) * tn)),
+                       dim3(256 * NWM), (TileLds<TN, TM, NWM, NS, NW>::kBytes), st, p, tn);
+    return hipGetLastError();
+}
+
+// Which kernel, from the expected rows R' of an expert that has any and the workgroups (items) that each would have; us
+// on MI355X in graphs of calls, operands rotating through more than the 256 MB memory-side cache:
+//   The ring kernel where one of its forms has at most a workgroup for each CU: of those the one that copies least
+//     beside a CU's share of the weights, the larger tile where two do alike. M x N x K: 1 x 4096 x 4096 5.5 with 16 x
+//     16 outputs to a workgroup, 6.6 with 16 x 32; 64 x 4096 x 4096 8.6 with 32 x 32, 11.0 with 32 x 64; 256 x 4096 x
+//     4096 15.0 with 64 x 64, 18.1 with 32 x 64; 512 x 4096 x 4096 21.5 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
+//     tile kernel; 333 x 2112 x 7168 22.1 against 41. Half of K to a wave instead of a quarter where K is short: 333 x
+//     2112 x 768 6.5 against 8.1. With up to 16 rows of a dense product at any number of columns.
+//   experts with R' <= 5 (SwiGLU), 10 (else): the streaming kernel, a quarter of K to a wave, half of K below 2048: 128
+//     experts, 2048 -> 2 x 768, 64 tokens 73.5 against 76.5 in the tile kernel, 768 -> 2048 with 16 tokens 26.8, with
+//     quarters 29.0
+//   R' <= 40: tiles of 128 x 64 (weight rows x tokens): 32 rows for each of 128 experts, 2048 -> 2 x 768, 76.5, as with 256 x
+//     64; 81.8 with 256 x 128
+//   above: 256 x 192 or 256 x 128, by the rounds of tiles over the CUs, a round of the larger ones taking 1.32 times as
+//     long: 8192 x 14336 x 4096 469 and 494, 4096 x 4096 x 7168 145 and 119; 256 x 64 where 256 x 128 leaves CUs idle (1024 x
+//     4096 x 4096 27.5 against 33.4). binary32 results take no larger tile than 256 x 128, whose registers hold the
+//     widened codes.
 template <int KIND, bool F32>
 hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 {
+    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
+    constexpr double kCus = 256.0;
     const Load load(g);
-    if (load.per <= 16.0)
-        return launch_stream<KIND, F32, 1, 2, 4, 2>(g, p, st);
-    return launch_stream<KIND, F32, 4, 2, 4, 2>(g, p, st);
+    const double per = load.per;
+    auto rounds = [&](int BN, int BM) { return ceil(load.items(BN, BM) / kCus); };
+    // the ring kernel's forms, larger tiles first: rows, weight rows, waves along the weights
+    struct Ring {
+        int rows, weights, wn;
+    };
+    constexpr Ring kRing[] = {{64, 128, 2}, {64, 64, 1}, {32, 128, 2}, {32, 64, 1}, {32, 32, 1}, {16, 128, 2}, {16, 64, 2}, {16, 32, 1}, {16, 16, 1}};
+    const bool short_k = g.K < 2048;
+    int best = -1;
+    double least = 0.0;
+    for (int i = 0; i < (SW ? 8 : 9); ++i) {
+        const Ring &r = kRing[i];
+        if ((r.rows > 16 && per <= r.rows / 2) || (short_k && r.wn == 1))
+            continue;
+        const double n = rounds(r.weights, r.rows), cost = n * (r.weights + r.rows * r.wn);
+        if ((n <= 1.0 || (!g.offsets && per <= 16.0)) && (best < 0 || cost < least)) {
+            best = i;
+            least = cost;
+        }
+    }
+    switch (best) {
+    case 0: return launch_ring<KIND, F32, 4, 4, 2, 2>(g, p, st);
+    case 1: return launch_ring<KIND, F32, 4, 4, 4, 2>(g, p, st);
+    case 2: return launch_ring<KIND, F32, 2, 4, 2, 2>(g, p, st);
+    case 3: return launch_ring<KIND, F32, 2, 4, 4, 2>(g, p, st);
+    case 4: return launch_ring<KIND, F32, 2, 2, 4, 2>(g, p, st);
+    case 5: return launch_ring<KIND, F32, 1, 4, 2, 2>(g, p, st);
+    case 6: return launch_ring<KIND, F32, 1, 2, 2, 2>(g, p, st);
+    case 7: return launch_ring<KIND, F32, 1, 2, 4, 2>(g, p, st);
+    case 8:
+        if constexpr (!SW)
+            return launch_ring<KIND, F32, 1, 1, 4, 4>(g, p, st);
+    }
+    if (g.offsets && per <= (SW ? 5.0 : 10.0))
+        return short_k ? launch_stream<KIND, F32, 1, 2, 2, 2>(g, p, st) : launch_stream<KIND, F32, 1, 2, 4, 2>(g, p, st);
+    if (per <= 40.0)
+        return launch_tile<KIND, F32, 2, 4, 1, 3, 3>(g, p, st);
+    if constexpr (!F32)
+        if (1.32 * rounds(256, 192) < rounds(256, 128))
+            return launch_tile<KIND, F32, 4, 6, 2, 3, 2>(g, p, st);
+    return load.items(256, 128) >= 192.0 ? launch_tile<KIND, F32, 4, 8, 1, 3, 3>(g, p, st)
+                                         : launch_tile<KIND, F32, 4, 4, 1, 3, 3>(g, p, st);
 }
 
 }  // namespace
