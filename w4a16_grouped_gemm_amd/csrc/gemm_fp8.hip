@@ -557,51 +557,59 @@ hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 }
 
 // ---------------------------------------------------------------------------
-// Many rows per expert: a workgroup of 4 NWM waves computes 64 TN weight rows x
-// 16 TM NWM tokens, a wave 16 TN rows x 16 TM tokens. Both pass through LDS, a
-// group of K (128 bytes) to a stage: the tokens' fragments are read as they are
-// needed, NS stages deep, the weights' a stage ahead into registers, which leaves
-// their place to the group after next. The tokens' scales follow 16 bytes (four
-// groups) at a time, the weights' are all loaded at the start.
+// Many rows per expert: a workgroup computes 64 TN weight rows x 16 TM tokens.
+// Four of its eight waves multiply, 16 TN rows by all the tokens each; the other
+// four copy both from memory straight to LDS, a group of K (128 bytes) to a stage
+// and kStages stages deep, and wait for the copies. A wave that multiplies issues
+// no copy: where it did, it stood behind the other waves' at the address unit (16
+// cycles a copy) while its matrix unit ran dry.
+//
+// The tokens' fragments are read from LDS as they are needed, the weights' a stage
+// ahead into registers, which leaves their place to the group after the next two.
+// The tokens' scales follow 16 bytes (four groups) at a time, the weights' are all
+// loaded at the start.
 //
 // A stage's rows are 128 bytes, eight 16-byte chunks each; row r keeps chunk c at
 // place c ^ ((r >> 1) & 7), so that the 64 lanes of a fragment read (16 rows x 4
-// chunks) meet no bank conflict. The copies go from memory straight to LDS, 16
-// bytes a lane, eight lanes to a row's 128 bytes: weights loaded by the lanes
-// that multiply them, each from a row of its own, came at 16 bytes a cycle and CU
-// (8192 x 14336 x 4096 495 us with that, 470 so).
+// chunks) meet no bank conflict. Eight lanes copy a row's 128 bytes: weights loaded
+// by the lanes that multiply them, each from a row of its own, come at 16 bytes a
+// cycle and CU, a quarter of this.
 //
 // A group's sums come out of the matrix unit kDelay instructions before their
 // multiply-adds onto the totals, which so run beside the next products.
 // ---------------------------------------------------------------------------
 constexpr int kDelay = 3;                             // MFMAs between a group's sum and its use
+constexpr int kStages = 3;                            // places for tokens and for weights
 constexpr int kMaxGroups = kMaxNormDim / kGroup;
 
-template <int TN, int TM, int NWM, int NS, int NW>
+template <int TN, int TM>
 struct TileLds {                                      // where things are, in bytes
-    static constexpr int kStage = 16 * TM * NWM * 128, kWeights = 64 * TN * 128;
-    static constexpr int kW = NS * kStage, kScale = kW + NW * kWeights;
-    static constexpr int kScaleCopies = (16 * TM * NWM + 63) / 64;       // 1 KiB each: 64 tokens' scales of four groups
+    static constexpr int kTokens = 16 * TM * 128, kWeights = 64 * TN * 128;   // of a stage
+    static constexpr int kW = kStages * kTokens, kScale = kW + kStages * kWeights;
+    static constexpr int kScaleCopies = (16 * TM + 63) / 64;   // 1 KiB each: 64 tokens' scales of four groups
     static constexpr int kWs = kScale + 2 * kScaleCopies * 1024, kBytes = kWs + 2 * kMaxGroups * 4 + 16;
 };
 
-template <int KIND, bool F32, int TN, int TM, int NWM, int NS, int NW>
-__global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8Args p, int tn)
+// The meeting of all waves: stores to LDS before it are seen behind it.
+__device__ __forceinline__ void meet()
 {
-    using S = TileLds<TN, TM, NWM, NS, NW>;
+    __builtin_amdgcn_sched_barrier(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int KIND, bool F32, int TN, int TM>
+__global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p, int tn)
+{
+    using S = TileLds<TN, TM>;
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
     constexpr int TG = SW ? TN / 2 : TN, H = SW ? 2 : 1;
-    constexpr int BM = 16 * TM * NWM, BC = 64 * TG, kThreads = 256 * NWM;   // tokens, output columns
-    constexpr int L = TM / 2, LW = 2 * TN / NWM;        // copies (loads) of a wave per stage: tokens, weights
-    constexpr int XR = TM % 8 == 0 ? 4 : TM % 6 == 0 ? 3 : 2;   // token fragments in registers
-    constexpr int M = TN * TM / 2;                      // MFMAs of half a stage
-    static_assert(TM % XR == 0 && M % (kDelay + 1) == 0 && TN * XR > kDelay, "rings");
-    static_assert(XR - 1 <= TM / 2, "the next stage's fragments are read in a stage's second half only");
-    static_assert(NS >= 3 && NS <= 5, "the first stages' scales are one copy");
+    constexpr int BM = 16 * TM, BC = 64 * TG;           // tokens, output columns
     extern __shared__ __align__(16) unsigned char s_dyn[];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int wn = wave / NWM, wm = wave % NWM;
-    const int m = lane & 15, q = lane >> 4;
+    const int wn = wave & 3;
     int e, r0, rows, nt;
     if (!find_tile(p, BM, tn, blockIdx.x, lane, e, r0, rows, nt))
         return;
@@ -610,95 +618,110 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
     rows = uniform(rows);
     const int cols = SW ? p.N / 2 : p.N;
     const int n0 = nt * BC, nw = n0 + wn * 16 * TG;     // the workgroup's and the wave's first column
-    const uint32_t K = (uint32_t)p.K;
     const int G = p.K / 128;
-
-    const __amdgpu_buffer_rsrc_t ri = index_rsrc(p);
-    const uint8_t *wbase = p.wq + (size_t)e * p.N * K;
-    lds_byte *lds = (lds_byte *)s_dyn;
-    // rows that this lane copies, a chunk of each, and the row whose scales it copies
-    int xrow[L], xidx[L];
+    // Stage g takes place g % kStages. The waves meet before stage 0 and in the middle of each stage g: then stage g + 1 is
+    // whole, every wave has read all tokens of stage g - 1, whose place takes those of stage g + 2, and has the weights of
+    // stage g in registers, whose place takes those of stage g + 3.
+    if (wave >= 4) {
+        constexpr int L = TM / 2, LW = 2 * TN;          // copies of a wave per stage: tokens, weights
+        const uint32_t K = (uint32_t)p.K;
+        const __amdgpu_buffer_rsrc_t ri = index_rsrc(p);
+        lds_byte *lds = (lds_byte *)s_dyn;
+        // rows that this lane copies, a chunk of each, and the row whose scales it copies
+        int xrow[L], xidx[L];
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const int row = (wave * L + j) * 8 + (lane >> 3);
-        xrow[j] = r0 + (row < rows ? row : rows - 1);
-        xidx[j] = load_index(ri, xrow[j]);
+        for (int j = 0; j < L; ++j) {
+            const int row = (wn * L + j) * 8 + (lane >> 3);
+            xrow[j] = r0 + (row < rows ? row : rows - 1);
+            xidx[j] = load_index(ri, xrow[j]);
+        }
+        int srow = wn * 64 + lane;
+        srow = r0 + (srow < rows ? srow : rows - 1);
+        const int sidx = load_index(ri, srow);
+        // row m of the wave's tile t is output (m / 4) 4 TG + 4 t + m % 4
+        const uint32_t chunk = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;   // of this lane's row in copies of rows 0 .. 7 of 16
+        uint32_t wo[LW], xo[L];
+#pragma unroll
+        for (int j = 0; j < LW; ++j) {
+            const int t = j / 2, r = (j & 1) * 8 + (lane >> 3);
+            int n = nw + (r >> 2) * 4 * TG + (t % TG) * 4 + (r & 3);
+            n = n < cols ? n : cols - 1;
+            wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + (chunk ^ (uint32_t)(j & 1) * 64);
+        }
+        const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * K, (uint32_t)p.N * K),
+                                     rx = make_rsrc(p.a, p.a_bytes), rxs = make_rsrc(p.as, p.a_bytes / 32);
+        auto copy_w = [&](int g, int at) {
+#pragma unroll
+            for (int j = 0; j < LW; ++j)
+                copy16(rw, lds + S::kW + at * S::kWeights + (wn * LW + j) * 1024, wo[j], g * 128);
+        };
+        // the weights set out before the tokens' rows are known
+        copy_w(0, 0);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            xo[j] = (uint32_t)act_row(p, xrow[j], xidx[j]) * K + (chunk ^ (uint32_t)((wn * L + j) & 1) * 64);
+        const uint32_t so = (uint32_t)act_row(p, srow, sidx) * G * 4;
+        auto copy_x = [&](int g, int at) {              // and the scales of groups g .. g + 3
+            if ((g & 3) == 0 && wn < S::kScaleCopies)
+                copy16(rxs, lds + S::kScale + ((g >> 2) & 1) * (S::kScaleCopies * 1024) + wn * 1024, so + g * 4, 0);
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                copy16(rx, lds + at * S::kTokens + (wn * L + j) * 1024, xo[j], g * 128);
+        };
+        copy_x(0, 0);
+        if (G > 1) {
+            copy_w(1, 1);
+            copy_x(1, 1);
+        }
+        if (G > 2)
+            copy_w(2, 2);
+        // In flight behind what a meeting needs: at the first one stage 1 and the weights of stage 2, later the weights of
+        // stage g + 2. Where K ends, fewer are, and all are waited for.
+        if (G > 2)
+            wait_for<L + 2 * LW>();
+        else
+            wait_for<0>();
+        meet();
+        int at = 0;                                     // place of stage g
+        for (int g = 0; g < G; ++g) {
+            if (g + 2 < G)
+                wait_for<LW>();
+            else
+                wait_for<0>();
+            meet();
+            if (g + 2 < G)
+                copy_x(g + 2, at == 0 ? 2 : at - 1);
+            if (g + 3 < G)
+                copy_w(g + 3, at);
+            at = at == 2 ? 0 : at + 1;
+        }
+        return;
     }
-    int srow = wave * 64 + lane;
-    srow = r0 + (srow < rows ? srow : rows - 1);
-    const int sidx = load_index(ri, srow);
+
+    constexpr int XR = TM % 8 == 0 ? 4 : 2;             // token fragments in registers
+    constexpr int M = TN * TM / 2;                      // MFMAs of half a stage
+    static_assert(TM % XR == 0 && M % (kDelay + 1) == 0 && TN * XR > kDelay, "rings");
+    static_assert(XR - 1 <= TM / 2, "the next stage's fragments are read in a stage's second half only");
+    const int m = lane & 15, q = lane >> 4;
     // the weights' scales of all groups: the (up to) two blocks of 128 rows that the workgroup's columns are in
     float *s_ws = reinterpret_cast<float *>(s_dyn + S::kWs);
-    constexpr int kWsLoads = 2 * kMaxGroups / kThreads;
-    float wsr[kWsLoads];
     {
         const __amdgpu_buffer_rsrc_t rws = scale_rsrc(p, e);
         const int last = (cols - 1) / 128;
         const int b0 = n0 / 128, b1 = SW ? b0 + cols / 128 : (b0 + 1 < last ? b0 + 1 : last);
-#pragma unroll
-        for (int i = 0; i < kWsLoads; ++i) {
-            const int at = threadIdx.x + kThreads * i, h = at >= G ? 1 : 0;
-            wsr[i] = load_f32(rws, at < 2 * G ? (uint32_t)((h ? b1 : b0) * G + at - h * G) * 4 : kOutOfRange, 0);
+        for (int i = threadIdx.x; i < 2 * G; i += 256) {
+            const int h = i >= G ? 1 : 0, g = i - h * G;
+            s_ws[h * kMaxGroups + g] = load_f32(rws, (uint32_t)((h ? b1 : b0) * G + g) * 4, 0);
         }
     }
     const int wsb = SW ? 0 : (nw < cols ? nw / 128 - n0 / 128 : 0) * kMaxGroups;
-    // the weights set out before the tokens' rows are known: row m of tile t is output (m / 4) 4 TG + 4 t + m % 4
-    const uint32_t chunk = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;   // of this lane's row in copies of rows 0 .. 7 of 16
-    uint32_t wo[LW];
-#pragma unroll
-    for (int j = 0; j < LW; ++j) {
-        const int i = wm * LW + j, t = i / 2, r = (i & 1) * 8 + (lane >> 3);
-        int n = nw + (r >> 2) * 4 * TG + (t % TG) * 4 + (r & 3);
-        n = n < cols ? n : cols - 1;
-        wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + (chunk ^ (uint32_t)(i & 1) * 64);
-    }
-    // one of the wave's copies of group g's weights to place `at` (past the last group of nothing, from an array of no bytes)
-    auto copy_w = [&](int j, int g, uint32_t at) {
-        copy16(make_rsrc(wbase, g < G ? (uint32_t)p.N * K : 0u), lds + S::kW + at + wn * (2048 * TN) + (wm * LW + j) * 1024,
-               wo[j], g < G ? g * 128 : 0);
-    };
-#pragma unroll
-    for (int j = 0; j < LW; ++j)
-        copy_w(j, 0, 0);
-    uint32_t xo[L];
-#pragma unroll
-    for (int j = 0; j < L; ++j)
-        xo[j] = (uint32_t)act_row(p, xrow[j], xidx[j]) * K + (chunk ^ (uint32_t)((wave * L + j) & 1) * 64);
-    const uint32_t so = (uint32_t)act_row(p, srow, sidx) * G * 4;
-    const __amdgpu_buffer_rsrc_t rxs = make_rsrc(p.as, p.a_bytes / 32);
-    auto copy_scales = [&](int g) {                     // groups g .. g + 3; for other g, and by other waves, nothing
-        if ((g & 3) == 0 && g < G && wave < S::kScaleCopies)
-            copy16(rxs, lds + S::kScale + ((g >> 2) & 1) * (S::kScaleCopies * 1024) + wave * 1024, so + g * 4, 0);
-    };
-    // one of the L copies of stage g's tokens to place `at`
-    auto copy_x = [&](int j, int g, uint32_t at) {
-        copy16(make_rsrc(p.a, g < G ? p.a_bytes : 0u), lds + at + (wave * L + j) * 1024, xo[j], g < G ? g * 128 : 0);
-    };
-    copy_scales(0);
-#pragma unroll
-    for (int g = 0; g < (NW > NS - 1 ? NW : NS - 1); ++g) {
-#pragma unroll
-        for (int j = 0; j < LW && g > 0 && g < NW; ++j)
-            copy_w(j, g, g * S::kWeights);
-#pragma unroll
-        for (int j = 0; j < L && g < NS - 1; ++j)
-            copy_x(j, g, g * S::kStage);
-    }
-#pragma unroll
-    for (int i = 0; i < kWsLoads; ++i) {
-        const int at = threadIdx.x + kThreads * i, h = at >= G ? 1 : 0;
-        if (at < 2 * G)
-            s_ws[h * kMaxGroups + at - h * G] = wsr[i];
-    }
-
     // fragment reads: lane l holds chunks l / 16 and l / 16 + 4 of row l % 16
     const uint32_t f0 = (uint32_t)(m * 128 + ((q ^ (m >> 1)) & 7) * 16);
     const uint32_t f1 = f0 ^ 64u;
-    const uint32_t x0 = wm * TM * 2048 + f0, x1 = wm * TM * 2048 + f1, xs0 = S::kScale + (wm * TM * 16 + m) * 16;
     Frag x[XR];
     float xs[XR], sc[XR][H];
     Frag w[2][TN];
-    // one of the 2 TN reads of group g's weight fragments
+    // one of the 2 TN reads of a group's weight fragments
     auto read_w = [&](Frag (&f)[TN], int j, uint32_t at) {
         const unsigned char *src = s_dyn + S::kW + at + wn * (2048 * TN) + j / 2 * 2048;
         if (j & 1)
@@ -709,11 +732,11 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
     // one of the three reads of token fragment b: its two chunks, its scales
     auto read_x = [&](int j, int b, uint32_t at, uint32_t scale_at) {
         if (j == 0)
-            x[b % XR].lo = *reinterpret_cast<const u32x4 *>(s_dyn + at + x0 + b * 2048);
+            x[b % XR].lo = *reinterpret_cast<const u32x4 *>(s_dyn + at + f0 + b * 2048);
         else if (j == 1)
-            x[b % XR].hi = *reinterpret_cast<const u32x4 *>(s_dyn + at + x1 + b * 2048);
+            x[b % XR].hi = *reinterpret_cast<const u32x4 *>(s_dyn + at + f1 + b * 2048);
         else
-            xs[b % XR] = *reinterpret_cast<const float *>(s_dyn + scale_at + xs0 + b * 256);
+            xs[b % XR] = *reinterpret_cast<const float *>(s_dyn + S::kScale + scale_at + m * 16 + b * 256);
     };
     floatx4 tot[TN][TM], c[kDelay + 1];
 #pragma unroll
@@ -736,13 +759,12 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
     };
     float wsv[H];
     uint32_t cur = 0, wcur = 0;                         // places of stage g
-    auto next_place = [&](uint32_t at) { return at == (NS - 1) * S::kStage ? 0u : at + S::kStage; };
     auto scale_place = [&](int g) { return (uint32_t)(((g >> 2) & 1) * (S::kScaleCopies * 1024) + (g & 3) * 4); };
     // Half a stage: products of token fragments [HALF TM / 2, ...), XR - 1 fragments read ahead (those of stage g + 1,
     // at `nxt`, behind the last). Between two products stand the multiply-adds of an earlier one and what there is to
-    // read or to copy, in this order: the compiler's own is full of waits.
-    auto half_stage = [&](auto half, const Frag (&f)[TN], int g, uint32_t nxt, auto copy, auto copies, auto read, auto reads) {
-        constexpr int HALF = decltype(half)::value, COPIES = decltype(copies)::value, READS = decltype(reads)::value;
+    // read, in this order: the compiler's own is full of waits.
+    auto half_stage = [&](auto half, const Frag (&f)[TN], int g, uint32_t nxt, auto read, auto reads) {
+        constexpr int HALF = decltype(half)::value, READS = decltype(reads)::value;
 #pragma unroll
         for (int k = 0; k < TM / 2; ++k) {
             const int b = HALF * TM / 2 + k, ahead = b + XR - 1;
@@ -757,9 +779,6 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
 #pragma unroll
                 for (int j = spread_to(at, READS, M); j < spread_to(at + 1, READS, M); ++j)
                     read(j);
-#pragma unroll
-                for (int j = spread_to(at, COPIES, M); j < spread_to(at + 1, COPIES, M); ++j)
-                    copy(j);
                 add((i + TN * TM - kDelay) % (TN * TM));
                 if (a == 0) {
 #pragma unroll
@@ -770,47 +789,26 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
             }
         }
     };
-    // Stage g. In its middle the wave waits for its copies of stage g + 1 and meets the other waves: then stage g + 1 and
-    // its weights are whole, every wave has read all of stage g - 1, whose place takes stage g + NS - 1, and has the
-    // weights of stage g in registers, whose place takes those of stage g + NW. Of the copies under way at the meeting,
-    // those that went out behind stage g + 1's stay so: with two places for weights, which then go before the tokens,
-    // the tokens of NS - 3 stages; with three, which go behind them, the last weights.
     using Half0 = std::integral_constant<int, 0>;
     using Half1 = std::integral_constant<int, 1>;
-    using None = std::integral_constant<int, 0>;
-    static_assert(NW == 2 || (NW == 3 && NS == 3), "what stays under way");
-    constexpr bool kWFirst = NW == 2;
-    constexpr int kStay = kWFirst ? (NS - 3) * L : LW;
     auto stage = [&](const Frag (&f)[TN], Frag (&fn)[TN], int g) {
-        const uint32_t nxt = next_place(cur), wnxt = wcur == (NW - 1) * S::kWeights ? 0u : wcur + S::kWeights;
-        half_stage(Half0(), f, g, nxt, [](int) {}, None(), [](int) {}, None());
-        wait_barrier<kStay>();
-        copy_scales(g + NS - 1);
-        const uint32_t to = cur >= S::kStage ? cur - S::kStage : (NS - 1) * S::kStage;
+        const uint32_t nxt = cur == 2 * S::kTokens ? 0u : cur + S::kTokens, wnxt = wcur == 2 * S::kWeights ? 0u : wcur + S::kWeights;
+        half_stage(Half0(), f, g, nxt, [](int) {}, std::integral_constant<int, 0>());
+        meet();
         float wsn[H];
 #pragma unroll
         for (int h = 0; h < H; ++h)
             wsn[h] = s_ws[wsb + h * kMaxGroups + g + 1];
-        half_stage(Half1(), f, g, nxt,
-                   [&](int j) {
-                       if (kWFirst ? j < LW : j >= L)
-                           copy_w(j - (kWFirst ? 0 : L), g + NW, wcur);
-                       else
-                           copy_x(j - (kWFirst ? LW : 0), g + NS - 1, to);
-                   },
-                   std::integral_constant<int, LW + L>(), [&](int j) { read_w(fn, j, wnxt); },
-                   std::integral_constant<int, 2 * TN>());
+        half_stage(Half1(), f, g, nxt, [&](int j) { read_w(fn, j, wnxt); }, std::integral_constant<int, 2 * TN>());
         cur = nxt;
         wcur = wnxt;
 #pragma unroll
         for (int h = 0; h < H; ++h)
             wsv[h] = wsn[h];
     };
-    // stage 0's tokens and weights are there; behind them went out the rest
-    constexpr int kBehind = (NS - 2) * L + (NW - 1) * LW;
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(kBehind) & ~(15u << 8));   // and the weights' scales written to LDS
-    wait_barrier<kBehind>();
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15u << 8));   // the weights' scales are in LDS
+    meet();
 #pragma unroll
     for (int j = 0; j < 2 * TN; ++j)
         read_w(w[0], j, 0);
@@ -834,7 +832,6 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
         stage(w[0], w[1], g);
         stage(w[1], w[0], g + 1);
     }
-    wait_for<0>();                                      // the copies past K, which write to LDS, end before the wave does
 #pragma unroll
     for (int i = TN * TM - kDelay; i < TN * TM; ++i)
         add(i);
@@ -842,7 +839,7 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
     // a lane's 4 TG outputs of a token are consecutive, four lanes make a run of 16 TG
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
-        const int t = (wm * TM + b) * 16 + m, n = nw + q * 4 * TG;
+        const int t = b * 16 + m, n = nw + q * 4 * TG;
         if (t >= rows || n >= cols)
             continue;
         const size_t at = (size_t)(r0 + t) * cols + n;
@@ -871,17 +868,16 @@ __global__ __launch_bounds__(256 * NWM, TM > 6 ? 1 : 2) void fp8_tile_kernel(Fp8
     }
 }
 
-template <int KIND, bool F32, int TN, int TM, int NWM, int NS, int NW>
+template <int KIND, bool F32, int TN, int TM>
 hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 {
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
-    constexpr int BM = 16 * TM * NWM, BC = 64 * (SW ? TN / 2 : TN);
+    constexpr int BM = 16 * TM, BC = 64 * (SW ? TN / 2 : TN), kBytes = TileLds<TN, TM>::kBytes;
     const int cols = SW ? g.N / 2 : g.N;
     const int tn = (cols + BC - 1) / BC;
-    allow_lds<decltype(fp8_tile_kernel<KIND, F32, TN, TM, NWM, NS, NW>), fp8_tile_kernel<KIND, F32, TN, TM, NWM, NS, NW>,
-              TileLds<TN, TM, NWM, NS, NW>::kBytes>();
-    hipLaunchKernelGGL((fp8_tile_kernel<KIND, F32, TN, TM, NWM, NS, NW>), dim3((unsigned)(chunks_at_most(g, BM) * tn)),
-                       dim3(256 * NWM), (TileLds<TN, TM, NWM, NS, NW>::kBytes), st, p, tn);
+    allow_lds<decltype(fp8_tile_kernel<KIND, F32, TN, TM>), fp8_tile_kernel<KIND, F32, TN, TM>, kBytes>();
+    hipLaunchKernelGGL((fp8_tile_kernel<KIND, F32, TN, TM>), dim3((unsigned)(chunks_at_most(g, BM) * tn)), dim3(512), kBytes,
+                       st, p, tn);
     return hipGetLastError();
 }
 
@@ -944,12 +940,11 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     if (g.offsets && per <= (SW ? 5.0 : 10.0))
         return short_k ? launch_stream<KIND, F32, 1, 2, 2, 2>(g, p, st) : launch_stream<KIND, F32, 1, 2, 4, 2>(g, p, st);
     if (per <= 40.0)
-        return launch_tile<KIND, F32, 2, 4, 1, 3, 3>(g, p, st);
+        return launch_tile<KIND, F32, 2, 4>(g, p, st);
     if constexpr (!F32)
-        if (1.32 * rounds(256, 192) < rounds(256, 128))
-            return launch_tile<KIND, F32, 4, 6, 2, 3, 2>(g, p, st);
-    return load.items(256, 128) >= 192.0 ? launch_tile<KIND, F32, 4, 8, 1, 3, 3>(g, p, st)
-                                         : launch_tile<KIND, F32, 4, 4, 1, 3, 3>(g, p, st);
+        if (load.items(256, 128) >= 192.0)
+            return launch_tile<KIND, F32, 4, 8>(g, p, st);
+    return launch_tile<KIND, F32, 4, 4>(g, p, st);
 }
 
 }  // namespace
