@@ -140,32 +140,52 @@ __device__ __forceinline__ void tile_of(int i, int tm, int tn, int &m, int &n)
     n = rest / gm;
 }
 
-// Workgroup b's tile of the tiles that there are (the grid holds as many as
-// there can be): XCD x (workgroups x, x + 8, ...) takes the x-th share of them,
-// so that those which share operands also share an L2. False where b has none.
+// The chunks that there are; of the last 256 experts' at most, c holds where they start.
 template <class P>
-__device__ __forceinline__ bool find_tile(const P &p, int CS, int tn, int b, int lane, int &e, int &r0, int &rows,
-                                          int &nt)
+__device__ __forceinline__ int count_chunks(const P &p, int CS, int lane, Chunks &c)
 {
-    Chunks c;
-    int tm = 0;
     if (!p.offsets)
-        tm = (p.max_rows + CS - 1) / CS;
-    else
-        for (int e0 = 0; e0 < p.E; e0 += 64 * kScan)
-            tm = scan_chunks<true>(p, CS, lane, e0, tm, c);
+        return (p.max_rows + CS - 1) / CS;
+    int tm = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64 * kScan)
+        tm = scan_chunks<true>(p, CS, lane, e0, tm, c);
+    return tm;
+}
+
+// Tile b of those that there are (tm chunks, tn column tiles; b counts up to as many as there can be): XCD x (tiles x, x +
+// 8, ... as workgroups are) takes the x-th share of them, so that those which share operands also share an L2. False past
+// XCD x's last.
+__device__ __forceinline__ bool have_tile(int tm, int tn, int b, int &mt, int &nt)
+{
     const int total = tm * tn, per = total / kXcds, extra = total % kXcds;
     const int x = b % kXcds, ix = b / kXcds;
     if (ix >= per + (x < extra ? 1 : 0))
         return false;
-    int mt;
     tile_of(x * per + (x < extra ? x : extra) + ix, tm, tn, mt, nt);
+    return true;
+}
+
+template <class P>
+__device__ __forceinline__ bool rows_of_tile(const P &p, int CS, int mt, int lane, const Chunks &c, int &e, int &r0,
+                                             int &rows)
+{
     if (!p.offsets)
         return dense_chunk(p, CS, mt, e, r0, rows);
     e = r0 = rows = 0;
     if (p.E <= 64 * kScan)
         return pick_chunk(p, CS, 0, mt, c, e, r0, rows);
     return find_chunk<true>(p, CS, mt, lane, e, r0, rows);
+}
+
+// The tile of workgroup b.
+template <class P>
+__device__ __forceinline__ bool find_tile(const P &p, int CS, int tn, int b, int lane, int &e, int &r0, int &rows,
+                                          int &nt)
+{
+    Chunks c;
+    const int tm = count_chunks(p, CS, lane, c);
+    int mt;
+    return have_tile(tm, tn, b, mt, nt) && rows_of_tile(p, CS, mt, lane, c, e, r0, rows);
 }
 
 // At most this many chunks of CS rows: the full ones and one part-filled per expert with rows.

@@ -566,8 +566,12 @@ hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //
 // The tokens' fragments are read from LDS as they are needed, the weights' a stage
 // ahead into registers, which leaves their place to the group after the next two.
-// The tokens' scales follow 16 bytes (four groups) at a time, the weights' are all
-// loaded at the start.
+// Scales come 16 bytes (four groups) at a time.
+//
+// A workgroup takes tile after tile, and the copies of the next one's first stages
+// go out under the last products of this one: neither the way from memory to the
+// first product nor the stores behind the last leave the memory or the matrix unit
+// idle between two tiles.
 //
 // A stage's rows are 128 bytes, eight 16-byte chunks each; row r keeps chunk c at
 // place c ^ ((r >> 1) & 7), so that the 64 lanes of a fragment read (16 rows x 4
@@ -576,18 +580,28 @@ hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 // cycle and CU, a quarter of this.
 //
 // A group's sums come out of the matrix unit kDelay instructions before their
-// multiply-adds onto the totals, which so run beside the next products.
+// multiply-adds onto the totals, which so run beside the next products: with one
+// instead of three 4096 x 4096 x 7168 takes 131 us instead of 115.
+//
+// us, tiles of 256 x 128: 4096 x 4096 x 7168 115 (2.1 PFLOP/s), 8192 x 8192 x 8192
+// 482 (2.3), 8192 x 14336 x 4096 452, with a tile to a workgroup 465; 2048 rows on 32
+// experts, 7168 -> 2 x 2048, 180 (940 MB of weights at 5.2 TB/s), 2048 -> 7168 108,
+// with a tile to a workgroup 186 and 111. The large ones are bound by the copies:
+// without them (the operands of the first three groups over and over) the first
+// three take 91, 374 and 364, at the clock that the matrix unit holds; all copies
+// from L2 instead of memory gain 6%.
 // ---------------------------------------------------------------------------
 constexpr int kDelay = 3;                             // MFMAs between a group's sum and its use
 constexpr int kStages = 3;                            // places for tokens and for weights
-constexpr int kMaxGroups = kMaxNormDim / kGroup;
+constexpr int kTilesAhead = 4;                        // groups that K must have where a workgroup takes several tiles
 
 template <int TN, int TM>
 struct TileLds {                                      // where things are, in bytes
     static constexpr int kTokens = 16 * TM * 128, kWeights = 64 * TN * 128;   // of a stage
     static constexpr int kW = kStages * kTokens, kScale = kW + kStages * kWeights;
-    static constexpr int kScaleCopies = (16 * TM + 63) / 64;   // 1 KiB each: 64 tokens' scales of four groups
-    static constexpr int kWs = kScale + 2 * kScaleCopies * 1024, kBytes = kWs + 2 * kMaxGroups * 4 + 16;
+    // scales of four groups: 1 KiB for 64 tokens each, 1 KiB for the weights; three places, as a tile's last may serve one stage
+    static constexpr int kScaleCopies = (16 * TM + 63) / 64, kScales = (kScaleCopies + 1) * 1024;
+    static constexpr int kTile = kScale + 3 * kScales, kBytes = kTile + 2 * 16;
 };
 
 // The meeting of all waves: stores to LDS before it are seen behind it.
@@ -610,92 +624,154 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
     extern __shared__ __align__(16) unsigned char s_dyn[];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wn = wave & 3;
-    int e, r0, rows, nt;
-    if (!find_tile(p, BM, tn, blockIdx.x, lane, e, r0, rows, nt))
-        return;
-    e = uniform(e);
-    r0 = uniform(r0);
-    rows = uniform(rows);
     const int cols = SW ? p.N / 2 : p.N;
-    const int n0 = nt * BC, nw = n0 + wn * 16 * TG;     // the workgroup's and the wave's first column
     const int G = p.K / 128;
-    // Stage g takes place g % kStages. The waves meet before stage 0 and in the middle of each stage g: then stage g + 1 is
-    // whole, every wave has read all tokens of stage g - 1, whose place takes those of stage g + 2, and has the weights of
-    // stage g in registers, whose place takes those of stage g + 3.
+    // Tile i of this workgroup for the waves that multiply: first row, rows, column tile, whether another follows
+    struct Tile {
+        int r0, rows, nt, more;
+    };
+    Tile *s_tile = reinterpret_cast<Tile *>(s_dyn + S::kTile);      // tile i in place i % 2
+    // Stage s, counted over all tiles, takes place s % kStages. The waves meet before the first stage and in the middle of
+    // each stage s: then stage s + 1 is whole, every wave has read all tokens of stage s - 1, whose place takes those of
+    // stage s + 2, and has the weights of stage s in registers, whose place takes those of stage s + 3.
     if (wave >= 4) {
         constexpr int L = TM / 2, LW = 2 * TN;          // copies of a wave per stage: tokens, weights
         const uint32_t K = (uint32_t)p.K;
         const __amdgpu_buffer_rsrc_t ri = index_rsrc(p);
         lds_byte *lds = (lds_byte *)s_dyn;
-        // rows that this lane copies, a chunk of each, and the row whose scales it copies
-        int xrow[L], xidx[L];
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int row = (wn * L + j) * 8 + (lane >> 3);
-            xrow[j] = r0 + (row < rows ? row : rows - 1);
-            xidx[j] = load_index(ri, xrow[j]);
-        }
-        int srow = wn * 64 + lane;
-        srow = r0 + (srow < rows ? srow : rows - 1);
-        const int sidx = load_index(ri, srow);
-        // row m of the wave's tile t is output (m / 4) 4 TG + 4 t + m % 4
-        const uint32_t chunk = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;   // of this lane's row in copies of rows 0 .. 7 of 16
-        uint32_t wo[LW], xo[L];
-#pragma unroll
-        for (int j = 0; j < LW; ++j) {
-            const int t = j / 2, r = (j & 1) * 8 + (lane >> 3);
-            int n = nw + (r >> 2) * 4 * TG + (t % TG) * 4 + (r & 3);
-            n = n < cols ? n : cols - 1;
-            wo[j] = (uint32_t)(n + (SW && t >= TG ? cols : 0)) * K + (chunk ^ (uint32_t)(j & 1) * 64);
-        }
-        const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * K, (uint32_t)p.N * K),
-                                     rx = make_rsrc(p.a, p.a_bytes), rxs = make_rsrc(p.as, p.a_bytes / 32);
-        auto copy_w = [&](int g, int at) {
-#pragma unroll
-            for (int j = 0; j < LW; ++j)
-                copy16(rw, lds + S::kW + at * S::kWeights + (wn * LW + j) * 1024, wo[j], g * 128);
+        Chunks chunks;
+        const int tm = uniform(count_chunks(p, BM, lane, chunks));
+        // where a tile's copies read from: this lane's rows of weights and tokens, a chunk of each, and of scales
+        struct From {
+            int e;
+            uint32_t w[LW], x[L], ws, xs;
         };
-        // the weights set out before the tokens' rows are known
-        copy_w(0, 0);
+        const uint32_t chunk = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;   // of this lane's row in copies of rows 0 .. 7 of 16
+        int xrow[L + 1], xidx[L + 1];                   // rows whose tokens this lane copies; whose scales
+        auto find = [&](int b, Tile &t, From &f) {      // tile b: what follows from its place alone, and the index on its way
+            int mt = 0, nt = 0, e, r0, rows, next_m, next_n;
+            t = Tile{0, 0, -1, 0};
+            if (!have_tile(tm, tn, b, mt, nt))
+                return false;
+            if (!rows_of_tile(p, BM, mt, lane, chunks, e, r0, rows))
+                e = r0 = rows = 0;                      // not reached: offsets are clamped; would compute and store nothing
+            f.e = uniform(e);
+            t.r0 = uniform(r0);
+            t.rows = uniform(rows);
+            t.nt = nt;
+            const int row1 = t.rows > 1 ? t.rows - 1 : 0;
+            t.more = have_tile(tm, tn, b + (int)gridDim.x, next_m, next_n) ? 1 : 0;
 #pragma unroll
-        for (int j = 0; j < L; ++j)
-            xo[j] = (uint32_t)act_row(p, xrow[j], xidx[j]) * K + (chunk ^ (uint32_t)((wn * L + j) & 1) * 64);
-        const uint32_t so = (uint32_t)act_row(p, srow, sidx) * G * 4;
-        auto copy_x = [&](int g, int at) {              // and the scales of groups g .. g + 3
-            if ((g & 3) == 0 && wn < S::kScaleCopies)
-                copy16(rxs, lds + S::kScale + ((g >> 2) & 1) * (S::kScaleCopies * 1024) + wn * 1024, so + g * 4, 0);
+            for (int j = 0; j <= L; ++j) {
+                const int row = j < L ? (wn * L + j) * 8 + (lane >> 3) : wn * 64 + lane;
+                xrow[j] = t.r0 + (row < row1 ? row : row1);
+                xidx[j] = load_index(ri, xrow[j]);
+            }
+            // row m of a multiplying wave's tile a is output (m / 4) 4 TG + 4 a + m % 4
+            const int nw = nt * BC + wn * 16 * TG;
+#pragma unroll
+            for (int j = 0; j < LW; ++j) {
+                const int a = j / 2, r = (j & 1) * 8 + (lane >> 3);
+                int n = nw + (r >> 2) * 4 * TG + (a % TG) * 4 + (r & 3);
+                n = n < cols ? n : cols - 1;
+                f.w[j] = (uint32_t)(n + (SW && a >= TG ? cols : 0)) * K + (chunk ^ (uint32_t)(j & 1) * 64);
+            }
+            // the (up to) two blocks of 128 weight rows that the tile's columns are in, one to the even lanes, one to the odd
+            const int last = (cols - 1) / 128, b0 = nt * BC / 128;
+            const int b1 = SW ? b0 + cols / 128 : (b0 + 1 < last ? b0 + 1 : last);
+            f.ws = (uint32_t)((lane & 1 ? b1 : b0) * G) * 4;
+            return true;
+        };
+        auto find_rows = [&](From &f) {                 // the rest, of the index
 #pragma unroll
             for (int j = 0; j < L; ++j)
-                copy16(rx, lds + at * S::kTokens + (wn * L + j) * 1024, xo[j], g * 128);
+                f.x[j] = (uint32_t)act_row(p, xrow[j], xidx[j]) * K + (chunk ^ (uint32_t)((wn * L + j) & 1) * 64);
+            f.xs = (uint32_t)act_row(p, xrow[L], xidx[L]) * G * 4;
         };
-        copy_x(0, 0);
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, p.a_bytes), rxs = make_rsrc(p.as, p.a_bytes / 32);
+        auto copy_w = [&](const From &f, int g, int at) {
+            const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)f.e * p.N * K, (uint32_t)p.N * K);
+#pragma unroll
+            for (int j = 0; j < LW; ++j)
+                copy16(rw, lds + S::kW + at * S::kWeights + (wn * LW + j) * 1024, f.w[j], g * 128);
+        };
+        int scale_at = 2 * S::kScales;                  // the last place that scales went to
+        auto copy_x = [&](const From &f, int g, int at) {   // and the scales of groups g .. g + 3
+            if ((g & 3) == 0) {
+                scale_at = scale_at == 2 * S::kScales ? 0 : scale_at + S::kScales;
+                if (wn < S::kScaleCopies)
+                    copy16(rxs, lds + S::kScale + scale_at + wn * 1024, f.xs + g * 4, 0);
+                else if (wn == 3)
+                    copy16(scale_rsrc(p, f.e), lds + S::kScale + scale_at + S::kScaleCopies * 1024, f.ws + g * 4, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                copy16(rx, lds + at * S::kTokens + (wn * L + j) * 1024, f.x[j], g * 128);
+        };
+        Tile tile;
+        From from, next;
+        int b = blockIdx.x;
+        const bool any = find(b, tile, from);
+        if (wave == 4)
+            s_tile[0] = tile;
+        if (!any) {
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15u << 8));
+            meet();
+            return;
+        }
+        // the weights set out before the tokens' rows are known
+        copy_w(from, 0, 0);
+        find_rows(from);
+        copy_x(from, 0, 0);
         if (G > 1) {
-            copy_w(1, 1);
-            copy_x(1, 1);
+            copy_w(from, 1, 1);
+            copy_x(from, 1, 1);
         }
         if (G > 2)
-            copy_w(2, 2);
+            copy_w(from, 2, 2);
         // In flight behind what a meeting needs: at the first one stage 1 and the weights of stage 2, later the weights of
-        // stage g + 2. Where K ends, fewer are, and all are waited for.
+        // stage s + 2. Where the stages end, fewer are, and all are waited for.
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15u << 8));
         if (G > 2)
             wait_for<L + 2 * LW>();
         else
             wait_for<0>();
         meet();
-        int at = 0;                                     // place of stage g
-        for (int g = 0; g < G; ++g) {
-            if (g + 2 < G)
-                wait_for<LW>();
-            else
-                wait_for<0>();
-            meet();
-            if (g + 2 < G)
-                copy_x(g + 2, at == 0 ? 2 : at - 1);
-            if (g + 3 < G)
-                copy_w(g + 3, at);
-            at = at == 2 ? 0 : at + 1;
+        int at = 0;                                     // place of stage s
+        for (int i = 1;; ++i) {
+            const bool more = tile.more;
+            for (int g = 0; g < G; ++g) {
+                if (g + 2 < G || more)
+                    wait_for<LW>();
+                else
+                    wait_for<0>();
+                meet();
+                if (more) {                             // then G >= kTilesAhead: both steps come before the next tile's first copy
+                    if (g == 0) {
+                        b += gridDim.x;
+                        find(b, tile, next);
+                        if (wave == 4)
+                            s_tile[i & 1] = tile;
+                        __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15u << 8));
+                    }
+                    if (g == 1)
+                        find_rows(next);
+                }
+                const int at2 = at == 0 ? 2 : at - 1;
+                if (g + 2 < G)
+                    copy_x(from, g + 2, at2);
+                else if (more)
+                    copy_x(next, g + 2 - G, at2);
+                if (g + 3 < G)
+                    copy_w(from, g + 3, at);
+                else if (more)
+                    copy_w(next, g + 3 - G, at);
+                at = at == 2 ? 0 : at + 1;
+            }
+            if (!more)
+                return;
+            from = next;
         }
-        return;
     }
 
     constexpr int XR = TM % 8 == 0 ? 4 : 2;             // token fragments in registers
@@ -703,18 +779,6 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
     static_assert(TM % XR == 0 && M % (kDelay + 1) == 0 && TN * XR > kDelay, "rings");
     static_assert(XR - 1 <= TM / 2, "the next stage's fragments are read in a stage's second half only");
     const int m = lane & 15, q = lane >> 4;
-    // the weights' scales of all groups: the (up to) two blocks of 128 rows that the workgroup's columns are in
-    float *s_ws = reinterpret_cast<float *>(s_dyn + S::kWs);
-    {
-        const __amdgpu_buffer_rsrc_t rws = scale_rsrc(p, e);
-        const int last = (cols - 1) / 128;
-        const int b0 = n0 / 128, b1 = SW ? b0 + cols / 128 : (b0 + 1 < last ? b0 + 1 : last);
-        for (int i = threadIdx.x; i < 2 * G; i += 256) {
-            const int h = i >= G ? 1 : 0, g = i - h * G;
-            s_ws[h * kMaxGroups + g] = load_f32(rws, (uint32_t)((h ? b1 : b0) * G + g) * 4, 0);
-        }
-    }
-    const int wsb = SW ? 0 : (nw < cols ? nw / 128 - n0 / 128 : 0) * kMaxGroups;
     // fragment reads: lane l holds chunks l / 16 and l / 16 + 4 of row l % 16
     const uint32_t f0 = (uint32_t)(m * 128 + ((q ^ (m >> 1)) & 7) * 16);
     const uint32_t f1 = f0 ^ 64u;
@@ -736,34 +800,25 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
         else if (j == 1)
             x[b % XR].hi = *reinterpret_cast<const u32x4 *>(s_dyn + at + f1 + b * 2048);
         else
-            xs[b % XR] = *reinterpret_cast<const float *>(s_dyn + S::kScale + scale_at + m * 16 + b * 256);
+            xs[b % XR] = *reinterpret_cast<const float *>(s_dyn + scale_at + m * 16 + b * 256);
     };
     floatx4 tot[TN][TM], c[kDelay + 1];
-#pragma unroll
-    for (int a = 0; a < TN; ++a)
-#pragma unroll
-        for (int b = 0; b < TM; ++b)
-            tot[a][b] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i <= kDelay; ++i)
-        c[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int b = 0; b < XR; ++b)
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-            sc[b][h] = 0.f;
     auto add = [&](int i) {                             // product i of a stage onto its total, here and not where that is used
         const int a = i % TN, b = i / TN;
         add_scaled(tot[a][b], sc[b % XR][SW && a >= TG ? 1 : 0], c[i % (kDelay + 1)]);
         keep(tot[a][b]);
     };
     float wsv[H];
-    uint32_t cur = 0, wcur = 0;                         // places of stage g
-    auto scale_place = [&](int g) { return (uint32_t)(((g >> 2) & 1) * (S::kScaleCopies * 1024) + (g & 3) * 4); };
+    uint32_t cur = 0, wcur = 0, scur = S::kScale;       // places of stage g, and of its scales
+    auto read_ws = [&](float (&v)[H], int wsb, uint32_t scale_at) {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            v[h] = *reinterpret_cast<const float *>(s_dyn + S::kScaleCopies * 1024 + scale_at + (SW ? h : wsb) * 16);
+    };
     // Half a stage: products of token fragments [HALF TM / 2, ...), XR - 1 fragments read ahead (those of stage g + 1,
     // at `nxt`, behind the last). Between two products stand the multiply-adds of an earlier one and what there is to
     // read, in this order: the compiler's own is full of waits.
-    auto half_stage = [&](auto half, const Frag (&f)[TN], int g, uint32_t nxt, auto read, auto reads) {
+    auto half_stage = [&](auto half, const Frag (&f)[TN], uint32_t nxt, uint32_t snxt, auto read, auto reads) {
         constexpr int HALF = decltype(half)::value, READS = decltype(reads)::value;
 #pragma unroll
         for (int k = 0; k < TM / 2; ++k) {
@@ -775,7 +830,7 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
                 c[i % (kDelay + 1)] = group_sum(Operand<F32>(f[a]), xv);
 #pragma unroll
                 for (int j = spread_to(a, 3, TN); j < spread_to(a + 1, 3, TN); ++j)
-                    read_x(j, ahead % TM, ahead < TM ? cur : nxt, scale_place(ahead < TM ? g : g + 1));
+                    read_x(j, ahead % TM, ahead < TM ? cur : nxt, ahead < TM ? scur : snxt);
 #pragma unroll
                 for (int j = spread_to(at, READS, M); j < spread_to(at + 1, READS, M); ++j)
                     read(j);
@@ -791,24 +846,34 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
     };
     using Half0 = std::integral_constant<int, 0>;
     using Half1 = std::integral_constant<int, 1>;
+    int wsb, wsb_next;                                  // which of the tile's two blocks of weight rows the wave's are in
+    auto block_of = [&](int nt) {
+        const int n0 = nt * BC, nw = n0 + wn * 16 * TG;
+        return SW || nw >= cols ? 0 : nw / 128 - n0 / 128;
+    };
+    // the last stage of a tile reads ahead of the next one's first
     auto stage = [&](const Frag (&f)[TN], Frag (&fn)[TN], int g) {
         const uint32_t nxt = cur == 2 * S::kTokens ? 0u : cur + S::kTokens, wnxt = wcur == 2 * S::kWeights ? 0u : wcur + S::kWeights;
-        half_stage(Half0(), f, g, nxt, [](int) {}, std::integral_constant<int, 0>());
+        const bool turn = ((g + 1) & 3) == 0 || g + 1 == G;
+        const uint32_t s0 = scur - (uint32_t)(g & 3) * 4;
+        const uint32_t snxt = !turn ? scur + 4 : s0 == S::kScale + 2 * S::kScales ? (uint32_t)S::kScale : s0 + S::kScales;
+        half_stage(Half0(), f, nxt, snxt, [](int) {}, std::integral_constant<int, 0>());
         meet();
         float wsn[H];
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-            wsn[h] = s_ws[wsb + h * kMaxGroups + g + 1];
-        half_stage(Half1(), f, g, nxt, [&](int j) { read_w(fn, j, wnxt); }, std::integral_constant<int, 2 * TN>());
+        read_ws(wsn, g + 1 == G ? wsb_next : wsb, snxt);
+        half_stage(Half1(), f, nxt, snxt, [&](int j) { read_w(fn, j, wnxt); }, std::integral_constant<int, 2 * TN>());
         cur = nxt;
         wcur = wnxt;
+        scur = snxt;
 #pragma unroll
         for (int h = 0; h < H; ++h)
             wsv[h] = wsn[h];
     };
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~(15u << 8));   // the weights' scales are in LDS
     meet();
+    if (uniform(s_tile[0].nt) < 0)
+        return;
+    wsb = block_of(uniform(s_tile[0].nt));
 #pragma unroll
     for (int j = 0; j < 2 * TN; ++j)
         read_w(w[0], j, 0);
@@ -816,55 +881,78 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
     for (int b = 0; b < XR - 1; ++b)
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-            read_x(j, b, 0, 0);
+            read_x(j, b, 0, S::kScale);
+    read_ws(wsv, wsb, S::kScale);
+    for (int ti = 0;; ++ti) {
+        const int r0 = uniform(s_tile[ti & 1].r0), rows = uniform(s_tile[ti & 1].rows), nt = uniform(s_tile[ti & 1].nt),
+                  more = uniform(s_tile[ti & 1].more);
+        const int nw = nt * BC + wn * 16 * TG;          // the wave's first column
+        wsb = wsb_next = block_of(nt);
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-        wsv[h] = s_ws[wsb + h * kMaxGroups];
-    // stages in pairs, an odd one first: one way out of the loop, else the compiler holds the totals twice
-    int g = 0;
-    if (G & 1) {
+        for (int a = 0; a < TN; ++a)
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
-            w[1][t] = w[0][t];
-        stage(w[1], w[0], g++);
-    }
-    for (; g < G; g += 2) {
-        stage(w[0], w[1], g);
-        stage(w[1], w[0], g + 1);
-    }
+            for (int b = 0; b < TM; ++b)
+                tot[a][b] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = TN * TM - kDelay; i < TN * TM; ++i)
-        add(i);
-
-    // a lane's 4 TG outputs of a token are consecutive, four lanes make a run of 16 TG
+        for (int i = 0; i <= kDelay; ++i)
+            c[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < TM; ++b) {
-        const int t = b * 16 + m, n = nw + q * 4 * TG;
-        if (t >= rows || n >= cols)
-            continue;
-        const size_t at = (size_t)(r0 + t) * cols + n;
-        float v[4 * TG];
+        for (int b = 0; b < XR; ++b)
 #pragma unroll
-        for (int a = 0; a < TG; ++a)
+            for (int h = 0; h < H; ++h)
+                sc[b][h] = 0.f;
+        // stages in pairs, an odd one first: one way out of the loop, else the compiler holds the totals twice
+        int g = 0;
+        if (G & 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[4 * a + i] = tot[a][b][i];
-                if constexpr (SW)
-                    v[4 * a + i] = silu_fast(v[4 * a + i]) * tot[a + TG][b][i];
-            }
-        // N is a multiple of 16: where the first of a lane's 4 TG <= 16 outputs exists, all do
-#pragma unroll
-        for (int a = 0; a < 4 * TG; a += F32 ? 4 : 8) {
-            if constexpr (F32)
-                *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + at + a) = floatx4{v[a], v[a + 1], v[a + 2], v[a + 3]};
-            else if constexpr (4 * TG >= 8)
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + at + a) =
-                    u32x4{bf16_pair(v[a], v[a + 1]), bf16_pair(v[a + 2], v[a + 3]), bf16_pair(v[a + 4], v[a + 5]),
-                          bf16_pair(v[a + 6], v[a + 7])};
-            else
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + at + a) =
-                    u32x2{bf16_pair(v[a], v[a + 1]), bf16_pair(v[a + 2], v[a + 3])};
+            for (int t = 0; t < TN; ++t)
+                w[1][t] = w[0][t];
+            stage(w[1], w[0], g++);
         }
+        for (; g < G; g += 2) {
+            stage(w[0], w[1], g);
+            if (g + 2 == G && more)                     // written two stages ago or before
+                wsb_next = block_of(uniform(s_tile[(ti + 1) & 1].nt));
+            stage(w[1], w[0], g + 1);
+        }
+#pragma unroll
+        for (int i = TN * TM - kDelay; i < TN * TM; ++i)
+            add(i);
+
+        // a lane's 4 TG outputs of a token are consecutive, four lanes make a run of 16 TG
+        int me = m;
+        asm volatile("" : "+v"(me));                    // else the rows' numbers are held in registers through the loop
+#pragma unroll
+        for (int b = 0; b < TM; ++b) {
+            const int t = b * 16 + me, n = nw + q * 4 * TG;
+            if (t >= rows || n >= cols)
+                continue;
+            const size_t at = (size_t)(r0 + t) * cols + n;
+            float v[4 * TG];
+#pragma unroll
+            for (int a = 0; a < TG; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[4 * a + i] = tot[a][b][i];
+                    if constexpr (SW)
+                        v[4 * a + i] = silu_fast(v[4 * a + i]) * tot[a + TG][b][i];
+                }
+            // N is a multiple of 16: where the first of a lane's 4 TG <= 16 outputs exists, all do
+#pragma unroll
+            for (int a = 0; a < 4 * TG; a += F32 ? 4 : 8) {
+                if constexpr (F32)
+                    *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + at + a) = floatx4{v[a], v[a + 1], v[a + 2], v[a + 3]};
+                else if constexpr (4 * TG >= 8)
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.c) + at + a) =
+                        u32x4{bf16_pair(v[a], v[a + 1]), bf16_pair(v[a + 2], v[a + 3]), bf16_pair(v[a + 4], v[a + 5]),
+                              bf16_pair(v[a + 6], v[a + 7])};
+                else
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + at + a) =
+                        u32x2{bf16_pair(v[a], v[a + 1]), bf16_pair(v[a + 2], v[a + 3])};
+            }
+        }
+        if (!more)
+            return;
     }
 }
 
@@ -875,9 +963,12 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     constexpr int BM = 16 * TM, BC = 64 * (SW ? TN / 2 : TN), kBytes = TileLds<TN, TM>::kBytes;
     const int cols = SW ? g.N / 2 : g.N;
     const int tn = (cols + BC - 1) / BC;
+    // as many workgroups as run at one time (a multiple of the XCDs), each with its share of the tiles
+    constexpr long long kAtOnce = 256 * (kBytes * 2 <= 160 * 1024 ? 2 : 1);
+    const long long all = chunks_at_most(g, BM) * tn;
+    const long long grid = g.K >= kTilesAhead * 128 && all > kAtOnce ? kAtOnce : all;
     allow_lds<decltype(fp8_tile_kernel<KIND, F32, TN, TM>), fp8_tile_kernel<KIND, F32, TN, TM>, kBytes>();
-    hipLaunchKernelGGL((fp8_tile_kernel<KIND, F32, TN, TM>), dim3((unsigned)(chunks_at_most(g, BM) * tn)), dim3(512), kBytes,
-                       st, p, tn);
+    hipLaunchKernelGGL((fp8_tile_kernel<KIND, F32, TN, TM>), dim3((unsigned)grid), dim3(512), kBytes, st, p, tn);
     return hipGetLastError();
 }
 
@@ -892,12 +983,10 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //   experts with R' <= 5 (SwiGLU), 10 (else): the streaming kernel, a quarter of K to a wave, half of K below 2048: 128
 //     experts, 2048 -> 2 x 768, 64 tokens 73.5 against 76.5 in the tile kernel, 768 -> 2048 with 16 tokens 26.8, with
 //     quarters 29.0
-//   R' <= 40: tiles of 128 x 64 (weight rows x tokens): 32 rows for each of 128 experts, 2048 -> 2 x 768, 76.5, as with 256 x
-//     64; 81.8 with 256 x 128
-//   above: 256 x 192 or 256 x 128, by the rounds of tiles over the CUs, a round of the larger ones taking 1.32 times as
-//     long: 8192 x 14336 x 4096 469 and 494, 4096 x 4096 x 7168 145 and 119; 256 x 64 where 256 x 128 leaves CUs idle (1024 x
-//     4096 x 4096 27.5 against 33.4). binary32 results take no larger tile than 256 x 128, whose registers hold the
-//     widened codes.
+//   R' <= 40: tiles of 128 x 64 (weight rows x tokens): 32 rows for each of 128 experts, 2048 -> 2 x 768, 76.6; 81.8 with
+//     256 x 128
+//   above: 256 x 128, and 256 x 64 where that leaves CUs idle: 1024 x 4096 x 4096 27.5, with 256 x 128 33.4. binary32
+//     results, whose widened codes need the registers, always 256 x 64.
 template <int KIND, bool F32>
 hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 {
