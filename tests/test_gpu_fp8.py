@@ -90,6 +90,14 @@ def test_dense(M, N, K):
         assert torch.equal(out, ops.dense_gemm_fp8(a, s, w, ws, out_dtype=dtype))
 
 
+MANY_TILES = [(2048, 6160, K) for K in (384, 512, 640, 768, 896, 1024, 1152)]      # several to a workgroup from K = 512 on
+
+
+@pytest.mark.parametrize("M,N,K", MANY_TILES + [(250, 4080, 2176)])
+def test_dense_many_tiles(M, N, K):
+    test_dense(M, N, K)
+
+
 @pytest.mark.parametrize("M", [1, 9, 16])
 @pytest.mark.parametrize("N", [14336, 12304])
 @pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 1152, 2432])
@@ -105,7 +113,7 @@ def powers(g, *shape):
     return torch.exp2(torch.randint(-2, 2, shape, generator=g, device="cuda").float())
 
 
-EXACT = DENSE + [(1, 128, 65536), (40, 144, 65536), (500, 272, 33024), (8192, 272, 128), (192, 1024, 512), (191, 1024, 640),
+EXACT = DENSE + MANY_TILES + [(1, 128, 65536), (40, 144, 65536), (500, 272, 33024), (8192, 272, 128), (192, 1024, 512), (191, 1024, 640),
                  (193, 1024, 896), (2000, 4096, 1280), (5000, 6160, 256)]
 
 
@@ -191,6 +199,20 @@ def test_grouped(T, E, begin, L, k, H, I, mode):
             assert near(outs[F32][r], b.c, b.f32) and near(outs[B16][r], b.c, b.fp8 + b.c.abs() * 2.0 ** -8)
     # rows in permuted order give the gathered rows' results
     assert torch.equal(run(ops.W13_SWIGLU, xp.contiguous(), xsp, w13, s13, I, B16, None), gate_up)
+
+
+@pytest.mark.parametrize("T,I", [(4, 512), (24, 640), (24, 1280), (50, 1280)])
+def test_grouped_small_products(T, I):
+    """Outputs that a workgroup for each CU covers, with quarters of K: 16 x 16, 32 x 16, 32 x 32, 64 x 32."""
+    test_grouped(T, 4, 0, 4, 4, 2176, I, "uniform")
+
+
+@pytest.mark.parametrize("T,E,begin,L,k,H,I,mode", [
+    (1200, 300, 0, 300, 8, 640, 512, "uniform"), (1000, 300, 0, 300, 8, 512, 1280, "zipf"), (3000, 300, 0, 300, 8, 512, 768, "uniform"),
+    (2000, 100, 10, 60, 8, 768, 640, "zipf"), (4000, 3, 0, 3, 3, 896, 1024, "uniform")])
+def test_grouped_many_tiles(T, E, begin, L, k, H, I, mode):
+    """Several tiles to a workgroup, of different experts; more than 256 experts are scanned again for each."""
+    test_grouped(T, E, begin, L, k, H, I, mode)
 
 
 @pytest.mark.parametrize("H,I", [(128, 384), (640, 128), (640, 256), (640, 384), (768, 512), (896, 640), (1024, 768), (1920, 896),
