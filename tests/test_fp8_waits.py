@@ -61,7 +61,7 @@ def test_tile_kernel(tn, tm, tmp_path):
         assert {lx + 2 * lw, lw} <= waits(ins, "s_barrier") and 0 in waits(ins, None), sym
 
 
-RINGS = [(4, 4, 2, 2), (4, 4, 4, 2), (2, 4, 2, 2), (2, 4, 4, 2), (2, 2, 4, 2), (1, 4, 2, 2), (1, 2, 2, 2), (1, 2, 4, 2), (1, 1, 4, 4)]
+RINGS = [(4, 4, 2, 2), (4, 4, 4, 2), (2, 4, 2, 2), (2, 4, 4, 2), (2, 2, 4, 2), (1, 4, 2, 2), (1, 2, 2, 2), (1, 2, 4, 2), (1, 1, 4, 4), (1, 2, 1, 2)]
 
 
 @pytest.mark.parametrize("nsub,tpw,wk,depth", RINGS)

@@ -128,202 +128,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const Fp8Args &p, i
 }
 
 // ---------------------------------------------------------------------------
-// Few rows per expert: the weights are what such a call has to read, once. Each
-// wave streams its own weight rows from memory to registers, RING groups of 128
-// bytes of K ahead, and multiplies them with NSUB subtiles of 16 tokens, whose
-// rows it fetches the same way (they stay in the caches). WK waves of a
-// workgroup share a set of rows, each with its part of K, and add their sums in
-// the waves' order through LDS; else no LDS and no barrier.
-// ---------------------------------------------------------------------------
-template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING>
-__global__ __launch_bounds__(256, 2) void fp8_stream_kernel(Fp8Args p, int blocks)
-{
-    constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
-    constexpr int TG = SW ? TPW / 2 : TPW;              // tiles side by side: a lane's outputs are 4 TG consecutive ones
-    constexpr int WN = 4 / WK, H = SW ? 2 : 1;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int m = lane & 15, q = lane >> 4;
-    const int wn = wave / WK, wk = wave % WK;
-    const int chunk = blockIdx.x / blocks;
-    const int block = blockIdx.x - chunk * blocks;
-    int e, r0, rows;
-    if (!find_chunk<false>(p, 16 * NSUB, chunk, lane, e, r0, rows))
-        return;
-    e = uniform(e);
-    const int cols = SW ? p.N / 2 : p.N;                // outputs per row
-    const int n0 = (block * WN + wn) * 16 * TG;
-    if (WK == 1 && n0 >= cols)
-        return;
-    // weight row of lane row m in tile t: outputs n0 + (m / 4) 4 TG + 4 t + m % 4 (gate), the same + N / 2 (up)
-    uint32_t wo[TPW], xo[NSUB], so[NSUB];
-#pragma unroll
-    for (int t = 0; t < TPW; ++t) {
-        int n = n0 + (m >> 2) * 4 * TG + (t % TG) * 4 + (m & 3);
-        n = n < cols ? n : cols - 1;
-        if (SW && t >= TG)
-            n += cols;
-        wo[t] = (uint32_t)n * p.K + q * 16;
-    }
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)e * p.N * p.K, (uint32_t)p.N * p.K);
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, p.a_bytes), ri = index_rsrc(p);
-    const __amdgpu_buffer_rsrc_t rxs = make_rsrc(p.as, p.a_bytes / 32), rws = scale_rsrc(p, e);
-    // 16 TG columns from a multiple of 16 TG on are all of one block of 128
-    const int G = p.K / 128;
-    const uint32_t ws0 = (uint32_t)(n0 < cols ? n0 : cols - 1) / 128 * G * 4, ws1 = ws0 + (uint32_t)(cols / 128) * G * 4;
-    int row[NSUB], idx[NSUB];
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s) {
-        row[s] = r0 + (16 * s + m < rows ? 16 * s + m : rows - 1);
-        idx[s] = load_index(ri, row[s]);
-    }
-    floatx4 acc[NSUB][TPW];
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s)
-#pragma unroll
-        for (int t = 0; t < TPW; ++t)
-            acc[s][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-    Frag w[RING][TPW], x[RING][NSUB];
-    float sw[RING][H], sx[RING][NSUB];
-    auto load_w = [&](int j, int g, uint32_t past = 0) {
-#pragma unroll
-        for (int t = 0; t < TPW; ++t) {
-            w[j][t].lo = bload16(rw, wo[t] + past, g * 128);
-            w[j][t].hi = bload16(rw, wo[t] + past + 64, g * 128);
-        }
-        sw[j][0] = load_f32(rws, past, ws0 + g * 4);
-        if constexpr (SW)
-            sw[j][1] = load_f32(rws, past, ws1 + g * 4);
-    };
-    auto load_x = [&](int j, int g) {
-#pragma unroll
-        for (int s = 0; s < NSUB; ++s) {
-            x[j][s].lo = bload16(rx, xo[s], g * 128);
-            x[j][s].hi = bload16(rx, xo[s] + 64, g * 128);
-            sx[j][s] = load_f32(rxs, so[s], g * 4);
-        }
-    };
-    auto multiply = [&](int j) {
-#pragma unroll
-        for (int s = 0; s < NSUB; ++s) {
-            const Operand<F32> xv(x[j][s]);
-#pragma unroll
-            for (int t = 0; t < TPW; ++t)
-                add_scaled(acc[s][t], sx[j][s] * sw[j][SW && t >= TG ? 1 : 0], group_sum(Operand<F32>(w[j][t]), xv));
-        }
-    };
-    // n groups from g on are this wave's, in rounds of RING: while a round is multiplied the next one is on its way
-    int g = wk * G / WK, n = (wk + 1) * G / WK - g;
-    // The first round's weights set out before the tokens' rows are known; groups past a wave's last one are loaded
-    // from behind the array, which fetches nothing (a weight offset is below 2^31).
-#pragma unroll
-    for (int j = 0; j < RING; ++j)
-        load_w(j, g + j, j < n ? 0u : 1u << 31);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s) {
-        const int ar = act_row(p, row[s], idx[s]);
-        xo[s] = (uint32_t)ar * p.K + q * 16;
-        so[s] = (uint32_t)ar * G * 4;
-    }
-    if (n >= RING) {
-#pragma unroll
-        for (int j = 0; j < RING; ++j)
-            load_x(j, g + j);
-        for (; n >= 2 * RING; n -= RING, g += RING)
-#pragma unroll
-            for (int j = 0; j < RING; ++j) {
-                multiply(j);
-                load_w(j, g + RING + j);
-                load_x(j, g + RING + j);
-            }
-        n -= RING;
-#pragma unroll
-        for (int j = 0; j < RING; ++j) {
-            multiply(j);
-            if (j < n) {
-                load_w(j, g + RING + j);
-                load_x(j, g + RING + j);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < RING - 1; ++j)
-            if (j < n)
-                load_x(j, g + j);
-    }
-#pragma unroll
-    for (int j = 0; j < RING - 1; ++j)
-        if (j < n)
-            multiply(j);
-    if constexpr (WK > 1) {
-        __shared__ floatx4 s_part[WN][WK - 1][NSUB * TPW][64];
-#pragma unroll
-        for (int s = 0; s < NSUB; ++s)
-#pragma unroll
-            for (int t = 0; t < TPW; ++t)
-                if (wk > 0)
-                    s_part[wn][wk - 1][s * TPW + t][lane] = acc[s][t];
-        __syncthreads();
-        if (wk > 0)
-            return;
-#pragma unroll
-        for (int i = 0; i < WK - 1; ++i)
-#pragma unroll
-            for (int s = 0; s < NSUB; ++s)
-#pragma unroll
-                for (int t = 0; t < TPW; ++t)
-                    acc[s][t] += s_part[wn][i][s * TPW + t][lane];
-    }
-    const int nq = n0 + q * 4 * TG;
-#pragma unroll
-    for (int s = 0; s < NSUB; ++s) {
-        if (16 * s + m >= rows)
-            continue;
-        const size_t crow = (size_t)(r0 + 16 * s + m) * cols;
-#pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            const int n = nq + 4 * t;
-            if (n >= cols)
-                continue;
-            floatx4 v = acc[s][t];
-            if constexpr (SW)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = silu_fast(v[i]) * acc[s][t + TG][i];
-            if constexpr (F32)
-                *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + crow + n) = v;
-            else
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.c) + crow + n) =
-                    u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-        }
-    }
-}
-
-template <int KIND, bool F32, int NSUB, int TPW, int WK, int RING>
-hipError_t launch_stream(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
-{
-    constexpr int TG = KIND == MOE_GEMM_W13_SWIGLU ? TPW / 2 : TPW;
-    const int cols = KIND == MOE_GEMM_W13_SWIGLU ? g.N / 2 : g.N;
-    constexpr int BC = 16 * TG * (4 / WK);
-    const int blocks = (cols + BC - 1) / BC;
-    hipLaunchKernelGGL((fp8_stream_kernel<KIND, F32, NSUB, TPW, WK, RING>),
-                       dim3((unsigned)(chunks_at_most(g, 16 * NSUB) * blocks)), dim3(256), 0, st, p, blocks);
-    return hipGetLastError();
-}
-
-// ---------------------------------------------------------------------------
-// Few rows and few workgroups (dense products, a token's experts): the stream
-// through LDS. Each wave streams its own weight rows, TPW tiles of 16, and its chunk's NSUB subtiles
-// of 16 tokens through a part of LDS that no other wave sees, D groups of K ahead:
-// copies straight from memory, eight lanes to a row's 128 bytes, waited for by
+// Few rows or few workgroups: the weights are what such a call has to read, once.
+// Each wave streams its own weight rows, TPW tiles of 16, and its chunk's NSUB
+// subtiles of 16 tokens through a part of LDS that no other wave sees, D groups of K
+// ahead: copies straight from memory, eight lanes to a row's 128 bytes, waited for by
 // count, and no meeting of the waves. WK waves of a workgroup share a set of weight
 // rows, each with its part of K, and add their sums in the waves' order in the end.
 //
 // Loads to the registers of the lanes that multiply them take 16 bytes of a row
-// each and pass the cache one lane at a time: 16 x 14336 x 4096 17.1 us in the
-// streaming kernel and 14.0 here, 64 x 4096 x 4096 12.1 and 8.7. Where there are more
-// workgroups than the GPU holds at a time, LDS lets too few of them start early: 128
-// experts of 768 -> 2048 with a row each 26.8 us there, 31 here.
+// each and pass the cache one lane at a time: 16 x 14336 x 4096 17.1 us that way and
+// 14.0 here, 64 x 4096 x 4096 12.1 and 8.7. Where a wave takes all of K (experts with
+// a few rows each, more workgroups than run at a time), the weights come
+// non-temporally, which leaves the caches to the tokens: 128 experts with 4 rows each,
+// 2048 -> 2 x 768, 65 us (6.1 TB/s), in registers 76, there non-temporally 89 (the two
+// halves of a line are fetched apart and the second finds it gone); 4096 -> 2048 168
+// (6.3 TB/s) and 188.
 // ---------------------------------------------------------------------------
 // Copies and loads of a wave that went out behind those of a quad's group j when its turn comes: the groups after it,
 // and the next quads' scales in between.
@@ -391,7 +210,7 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
         const __amdgpu_buffer_rsrc_t rw = make_rsrc(wbase, k < end ? (uint32_t)p.N * p.K : 0u);
 #pragma unroll
         for (int j = 0; j < 2 * TPW; ++j)
-            copy16(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
+            copy16<WK == 1>(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
     };
     auto copy_x = [&](int k, int slot) {
         const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, k < end ? p.a_bytes : 0u);
@@ -566,7 +385,8 @@ hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //
 // The tokens' fragments are read from LDS as they are needed, the weights' a stage
 // ahead into registers, which leaves their place to the group after the next two.
-// Scales come 16 bytes (four groups) at a time.
+// Scales come 16 bytes (four groups) at a time. Weights that are read once, of experts
+// with one chunk of rows, come non-temporally.
 //
 // A workgroup takes tile after tile, and the copies of the next one's first stages
 // go out under the last products of this one: neither the way from memory to the
@@ -614,6 +434,13 @@ __device__ __forceinline__ void meet()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Whether expert e's rows are all in one chunk of CS: its weights are read once then.
+__device__ __forceinline__ bool read_once(const Fp8Args &p, int CS, int e)
+{
+    const uint32_t rows = p.offsets ? (uint32_t)p.offsets[e + 1] - (uint32_t)p.offsets[e] : (uint32_t)p.max_rows;
+    return uniform(rows <= (uint32_t)CS);
+}
+
 template <int KIND, bool F32, int TN, int TM>
 __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p, int tn)
 {
@@ -644,6 +471,7 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
         // where a tile's copies read from: this lane's rows of weights and tokens, a chunk of each, and of scales
         struct From {
             int e;
+            bool once;
             uint32_t w[LW], x[L], ws, xs;
         };
         const uint32_t chunk = (uint32_t)((lane & 7) ^ ((lane >> 4) & 3)) * 16;   // of this lane's row in copies of rows 0 .. 7 of 16
@@ -656,6 +484,7 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
             if (!rows_of_tile(p, BM, mt, lane, chunks, e, r0, rows))
                 e = r0 = rows = 0;                      // not reached: offsets are clamped; would compute and store nothing
             f.e = uniform(e);
+            f.once = read_once(p, BM, f.e);
             t.r0 = uniform(r0);
             t.rows = uniform(rows);
             t.nt = nt;
@@ -691,9 +520,15 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
         const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, p.a_bytes), rxs = make_rsrc(p.as, p.a_bytes / 32);
         auto copy_w = [&](const From &f, int g, int at) {
             const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.wq + (size_t)f.e * p.N * K, (uint32_t)p.N * K);
+            auto copies = [&](auto nt) {
 #pragma unroll
-            for (int j = 0; j < LW; ++j)
-                copy16(rw, lds + S::kW + at * S::kWeights + (wn * LW + j) * 1024, f.w[j], g * 128);
+                for (int j = 0; j < LW; ++j)
+                    copy16<decltype(nt)::value>(rw, lds + S::kW + at * S::kWeights + (wn * LW + j) * 1024, f.w[j], g * 128);
+            };
+            if (f.once)
+                copies(std::true_type());
+            else
+                copies(std::false_type());
         };
         int scale_at = 2 * S::kScales;                  // the last place that scales went to
         auto copy_x = [&](const From &f, int g, int at) {   // and the scales of groups g .. g + 3
@@ -980,9 +815,10 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //     4096 15.0 with 64 x 64, 18.1 with 32 x 64; 512 x 4096 x 4096 21.5 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
 //     tile kernel; 333 x 2112 x 7168 22.1 against 41. Half of K to a wave instead of a quarter where K is short: 333 x
 //     2112 x 768 6.5 against 8.1. With up to 16 rows of a dense product at any number of columns.
-//   experts with R' <= 5 (SwiGLU), 10 (else): the streaming kernel, a quarter of K to a wave, half of K below 2048: 128
-//     experts, 2048 -> 2 x 768, 64 tokens 73.5 against 76.5 in the tile kernel, 768 -> 2048 with 16 tokens 26.8, with
-//     quarters 29.0
+//   experts with R' <= 10 from K = 1024 on, or SwiGLU: the ring kernel with 16 x 32 weight rows to a wave, all of K (TB/s of
+//     all that is read and written, here and in tiles of 128 x 64): 2048 -> 2 x 768 with 1, 4, 8 and 16 rows for each of 128
+//     experts 5.8 and 5.4, 6.0 and 5.8, 6.1 and 5.8, 4.5 and 5.6; 2048 -> 2048 with 4 rows 6.3 and 6.0, 1024 -> 2048 5.9 and 5.7,
+//     768 -> 2048 5.2 and 5.7
 //   R' <= 40: tiles of 128 x 64 (weight rows x tokens): 32 rows for each of 128 experts, 2048 -> 2 x 768, 76.6; 81.8 with
 //     256 x 128
 //   above: 256 x 128, and 256 x 64 where that leaves CUs idle: 1024 x 4096 x 4096 27.5, with 256 x 128 33.4. binary32
@@ -1026,8 +862,8 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
         if constexpr (!SW)
             return launch_ring<KIND, F32, 1, 1, 4, 4>(g, p, st);
     }
-    if (g.offsets && per <= (SW ? 5.0 : 10.0))
-        return short_k ? launch_stream<KIND, F32, 1, 2, 2, 2>(g, p, st) : launch_stream<KIND, F32, 1, 2, 4, 2>(g, p, st);
+    if (g.offsets && per <= 10.0 && (SW || g.K >= 1024))
+        return launch_ring<KIND, F32, 1, 2, 1, 2>(g, p, st);
     if (per <= 40.0)
         return launch_tile<KIND, F32, 2, 4>(g, p, st);
     if constexpr (!F32)

@@ -16,10 +16,11 @@ constexpr uint32_t vmcnt_imm(int n)                   // s_waitcnt vmcnt(n), oth
     return (uint32_t)((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// 16 bytes per lane from memory to LDS: lane l's to dst + 16 l
+// 16 bytes per lane from memory to LDS: lane l's to dst + 16 l. NT: non-temporal, as bload16_codes.
+template <bool NT = false>
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, lds_byte *dst, uint32_t voff, uint32_t soff)
 {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, NT ? 2 : 0);
 }
 
 template <int N>
