@@ -152,6 +152,13 @@ __device__ __forceinline__ int count_chunks(const P &p, int CS, int lane, Chunks
     return tm;
 }
 
+// Where i of n lands so that XCD x, to which workgroups x, x + 8, ... go, takes the x-th share.
+__device__ __forceinline__ int xcd_share(int n, int i)
+{
+    const int per = n / kXcds, extra = n % kXcds, x = i % kXcds;
+    return x * per + (x < extra ? x : extra) + i / kXcds;
+}
+
 // Tile b of those that there are (tm chunks, tn column tiles; b counts up to as many as there can be): XCD x (tiles x, x +
 // 8, ... as workgroups are) takes the x-th share of them, so that those which share operands also share an L2. False past
 // XCD x's last.
@@ -161,7 +168,7 @@ __device__ __forceinline__ bool have_tile(int tm, int tn, int b, int &mt, int &n
     const int x = b % kXcds, ix = b / kXcds;
     if (ix >= per + (x < extra ? 1 : 0))
         return false;
-    tile_of(x * per + (x < extra ? x : extra) + ix, tm, tn, mt, nt);
+    tile_of(xcd_share(total, b), tm, tn, mt, nt);
     return true;
 }
 

@@ -143,6 +143,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const Fp8Args &p, i
 // 2048 -> 2 x 768, 65 us (6.1 TB/s), in registers 76, there non-temporally 89 (the two
 // halves of a line are fetched apart and the second finds it gone); 4096 -> 2048 168
 // (6.3 TB/s) and 188.
+//
+// Chunks of a dense product side by side on an XCD: 333 x 2112 x 7168 (33 column
+// blocks, which wander over the XCDs else) 22.1 -> 19.7 us; with the multiply-adds
+// three products behind their sums 19.5, binary32 results 24.4 -> 23.3, 256 x 4096 x
+// 4096 15.1 -> 14.8. What bounds it there is the way of the copies into LDS, 128 KiB
+// under way in each CU: weights that were touched ahead into L2 did not help.
 // ---------------------------------------------------------------------------
 // Copies and loads of a wave that went out behind those of a quad's group j when its turn comes: the groups after it,
 // and the next quads' scales in between.
@@ -164,8 +170,13 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int m = lane & 15, q = lane >> 4;
     const int wn = wave / WK, wk = wave % WK;
-    const int chunk = blockIdx.x / blocks;
-    const int block = blockIdx.x - chunk * blocks;
+    int chunk = blockIdx.x / blocks;
+    int block = blockIdx.x - chunk * blocks;
+    if (!p.offsets) {                                   // the chunks beside each other on one XCD, whose L2 keeps their weights
+        const int chunks = gridDim.x / blocks, i = xcd_share(gridDim.x, blockIdx.x);
+        block = i / chunks;
+        chunk = i - block * chunks;
+    }
     int e, r0, rows;
     if (!find_chunk<false>(p, 16 * NSUB, chunk, lane, e, r0, rows))
         return;
@@ -275,15 +286,28 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
 #pragma unroll
             for (int t = 0; t < TPW; ++t)
                 w[t] = fragment(SLOT, t);
+            constexpr int kLag = NSUB * TPW > 3 ? 3 : NSUB * TPW - 1;   // products between a group's sum and its use
+            floatx4 c[kLag + 1];
+            auto add = [&](int i) {
+                const int s = i / TPW, t = i % TPW;
+                add_scaled(acc[s][t], sc.x[s][J] * sc.w[SW && t >= TG ? 1 : 0][J], c[i % (kLag + 1)]);
+                keep(acc[s][t]);
+            };
 #pragma unroll
             for (int s = 0; s < NSUB; ++s) {
                 const Operand<F32> xv(fragment(SLOT, TPW + s));
 #pragma unroll
                 for (int t = 0; t < TPW; ++t) {
-                    add_scaled(acc[s][t], sc.x[s][J] * sc.w[SW && t >= TG ? 1 : 0][J], group_sum(Operand<F32>(w[t]), xv));
-                    keep(acc[s][t]);
+                    const int i = s * TPW + t;
+                    c[i % (kLag + 1)] = group_sum(Operand<F32>(w[t]), xv);
+                    if (i >= kLag)
+                        add(i - kLag);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
+#pragma unroll
+            for (int i = NSUB * TPW - kLag; i < NSUB * TPW; ++i)
+                add(i);
         }
         // every fragment has left LDS
         __builtin_amdgcn_sched_barrier(0);
@@ -812,8 +836,8 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //   The ring kernel where one of its forms has at most a workgroup for each CU: of those the one that copies least
 //     beside a CU's share of the weights, the larger tile where two do alike. M x N x K: 1 x 4096 x 4096 5.5 with 16 x
 //     16 outputs to a workgroup, 6.6 with 16 x 32; 64 x 4096 x 4096 8.6 with 32 x 32, 11.0 with 32 x 64; 256 x 4096 x
-//     4096 15.0 with 64 x 64, 18.1 with 32 x 64; 512 x 4096 x 4096 21.5 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
-//     tile kernel; 333 x 2112 x 7168 22.1 against 41. Half of K to a wave instead of a quarter where K is short: 333 x
+//     4096 14.8 with 64 x 64, 18.1 with 32 x 64; 512 x 4096 x 4096 21.2 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
+//     tile kernel; 333 x 2112 x 7168 19.5 against 41. Half of K to a wave instead of a quarter where K is short: 333 x
 //     2112 x 768 6.5 against 8.1. With up to 16 rows of a dense product at any number of columns.
 //   experts with R' <= 10 from K = 1024 on, or SwiGLU: the ring kernel with 16 x 32 weight rows to a wave, all of K (TB/s of
 //     all that is read and written, here and in tiles of 128 x 64): 2048 -> 2 x 768 with 1, 4, 8 and 16 rows for each of 128
