@@ -843,10 +843,12 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //     all that is read and written, here and in tiles of 128 x 64): 2048 -> 2 x 768 with 1, 4, 8 and 16 rows for each of 128
 //     experts 5.8 and 5.4, 6.0 and 5.8, 6.1 and 5.8, 4.5 and 5.6; 2048 -> 2048 with 4 rows 6.3 and 6.0, 1024 -> 2048 5.9 and 5.7,
 //     768 -> 2048 5.2 and 5.7
-//   R' <= 40: tiles of 128 x 64 (weight rows x tokens): 32 rows for each of 128 experts, 2048 -> 2 x 768, 76.6; 81.8 with
-//     256 x 128
-//   above: 256 x 128, and 256 x 64 where that leaves CUs idle: 1024 x 4096 x 4096 27.5, with 256 x 128 33.4. binary32
-//     results, whose widened codes need the registers, always 256 x 64.
+//   R' <= 28: tiles of 128 x 64 (weight rows x tokens): 25 and 32 rows for each of 128 experts, 2048 -> 2 x 768, 72.7 and
+//     75.4; 74.5 and 73.6 with 256 x 64; 80.1 and 78.1 with 256 x 128
+//   above: 256 x 128, but 256 x 64 where that takes no more rounds of the CUs: 1024 x 4096 x 4096 27.4, with 256 x 128 32;
+//     1536 x 4096 x 4096 43.3 and 34.1; 50 rows for each of 128 experts 87.1 and 81.7, where the few experts with more than
+//     64 make a round of their own: the rounds are those of R' and two standard deviations. binary32 results, whose
+//     widened codes need the registers, always 256 x 64: 4096 x 4096 x 4096 141, with 128 x 64 147.
 template <int KIND, bool F32>
 hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 {
@@ -888,10 +890,12 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     }
     if (g.offsets && per <= 10.0 && (SW || g.K >= 1024))
         return launch_ring<KIND, F32, 1, 2, 1, 2>(g, p, st);
-    if (per <= 40.0)
+    if (per <= 28.0)
         return launch_tile<KIND, F32, 2, 4>(g, p, st);
+    const double rows = g.offsets ? per + 2.0 * sqrt(per) : per, columns = load.items(256, 1) / ceil(per);
+    auto tall = [&](int BM) { return ceil(columns * ceil(rows / BM) / kCus); };
     if constexpr (!F32)
-        if (load.items(256, 128) >= 192.0)
+        if (tall(128) < tall(64))
             return launch_tile<KIND, F32, 4, 8>(g, p, st);
     return launch_tile<KIND, F32, 4, 4>(g, p, st);
 }
