@@ -61,7 +61,8 @@ def test_tile_kernel(tn, tm, tmp_path):
         assert {lx + 2 * lw, lw} <= waits(ins, "s_barrier") and 0 in waits(ins, None), sym
 
 
-RINGS = [(4, 4, 2, 2), (4, 4, 4, 2), (2, 4, 2, 2), (2, 4, 4, 2), (2, 2, 4, 2), (1, 4, 2, 2), (1, 2, 2, 2), (1, 2, 4, 2), (1, 1, 4, 4), (1, 2, 1, 2)]
+RINGS = [(4, 4, 2, 2), (3, 4, 2, 2), (5, 4, 4, 2), (4, 4, 4, 2), (3, 4, 4, 2), (2, 4, 2, 2), (2, 4, 4, 2), (2, 2, 4, 2),
+         (1, 4, 2, 2), (1, 2, 2, 2), (1, 2, 4, 2), (1, 1, 4, 4), (1, 2, 1, 2)]
 
 
 @pytest.mark.parametrize("nsub,tpw,wk,depth", RINGS)
@@ -69,7 +70,7 @@ def test_ring_kernel(nsub, tpw, wk, depth, tmp_path):
     cos = code_objects(tmp_path)
     copy = 2 * (tpw + nsub)
     for kind, f32 in KINDS:
-        if kind == 0 and tpw == 1:
+        if (kind == 0 and tpw == 1) or (f32 and nsub == 5):
             continue
         scales = nsub + (2 if kind == 0 else 1)
         sym = (f"_ZN3moe12_GLOBAL__N_115fp8_ring_kernelILi{kind}ELb{f32}ELi{nsub}ELi{tpw}ELi{wk}ELi{depth}EEEvNS0_"

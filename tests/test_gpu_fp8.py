@@ -93,7 +93,8 @@ def test_dense(M, N, K):
 MANY_TILES = [(2048, 6160, K) for K in (384, 512, 640, 768, 896, 1024, 1152)]      # several to a workgroup from K = 512 on
 
 
-@pytest.mark.parametrize("M,N,K", MANY_TILES + [(250, 4080, 2176)])
+@pytest.mark.parametrize("M,N,K", MANY_TILES + [(250, 4080, 2176), (333, 2112, 2432), (190, 4080, 2048), (350, 4096, 2176),
+                                                (300, 4000, 512), (450, 2544, 2304), (700, 2048, 2176)])
 def test_dense_many_tiles(M, N, K):
     test_dense(M, N, K)
 
@@ -201,9 +202,9 @@ def test_grouped(T, E, begin, L, k, H, I, mode):
     assert torch.equal(run(ops.W13_SWIGLU, xp.contiguous(), xsp, w13, s13, I, B16, None), gate_up)
 
 
-@pytest.mark.parametrize("T,I", [(4, 512), (24, 640), (24, 1280), (50, 1280)])
+@pytest.mark.parametrize("T,I", [(4, 512), (24, 640), (24, 1280), (36, 1280), (50, 1280), (70, 1920), (45, 2560), (60, 2560)])
 def test_grouped_small_products(T, I):
-    """Outputs that a workgroup for each CU covers, with quarters of K: 16 x 16, 32 x 16, 32 x 32, 64 x 32."""
+    """Outputs that a workgroup for each CU covers, with quarters and halves of K, in tiles of 16 to 80 rows."""
     test_grouped(T, 4, 0, 4, 4, 2176, I, "uniform")
 
 

@@ -836,9 +836,11 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //   The ring kernel where one of its forms has at most a workgroup for each CU: of those the one that copies least
 //     beside a CU's share of the weights, the larger tile where two do alike. M x N x K: 1 x 4096 x 4096 5.5 with 16 x
 //     16 outputs to a workgroup, 6.6 with 16 x 32; 64 x 4096 x 4096 8.6 with 32 x 32, 11.0 with 32 x 64; 256 x 4096 x
-//     4096 14.8 with 64 x 64, 18.1 with 32 x 64; 512 x 4096 x 4096 21.2 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
-//     tile kernel; 333 x 2112 x 7168 19.5 against 41. Half of K to a wave instead of a quarter where K is short: 333 x
-//     2112 x 768 6.5 against 8.1. With up to 16 rows of a dense product at any number of columns.
+//     4096 14.7 with 64 x 64, 18.1 with 32 x 64; 350 x 4096 x 4096 17.6 with 48 x 128, 20.2 with 64 x 128; 450 x 2560 x 4096
+//     15.7 with 80 x 64, 17.1 with 48 x 128; 512 x 4096 x 4096 21.0 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
+//     tile kernel; 333 x 2112 x 7168 18.0 with 48 x 64, 19.3 with 64 x 64 and 41 in the tile kernel. 80 rows of binary32
+//     results spill. Half of K to a wave instead of a quarter where K is short: 333 x 2112 x 768 6.5 against 8.1.
+//     With up to 16 rows of a dense product at any number of columns.
 //   experts with R' <= 10 from K = 1024 on, or SwiGLU: the ring kernel with 16 x 32 weight rows to a wave, all of K (TB/s of
 //     all that is read and written, here and in tiles of 128 x 64): 2048 -> 2 x 768 with 1, 4, 8 and 16 rows for each of 128
 //     experts 5.8 and 5.4, 6.0 and 5.8, 6.1 and 5.8, 4.5 and 5.6; 2048 -> 2048 with 4 rows 6.3 and 6.0, 1024 -> 2048 5.9 and 5.7,
@@ -861,13 +863,14 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     struct Ring {
         int rows, weights, wn;
     };
-    constexpr Ring kRing[] = {{64, 128, 2}, {64, 64, 1}, {32, 128, 2}, {32, 64, 1}, {32, 32, 1}, {16, 128, 2}, {16, 64, 2}, {16, 32, 1}, {16, 16, 1}};
+    constexpr Ring kRing[] = {{64, 128, 2}, {48, 128, 2}, {80, 64, 1}, {64, 64, 1}, {48, 64, 1}, {32, 128, 2},
+                              {32, 64, 1}, {32, 32, 1}, {16, 128, 2}, {16, 64, 2}, {16, 32, 1}, {16, 16, 1}};
     const bool short_k = g.K < 2048;
     int best = -1;
     double least = 0.0;
-    for (int i = 0; i < (SW ? 8 : 9); ++i) {
+    for (int i = 0; i < (SW ? 11 : 12); ++i) {
         const Ring &r = kRing[i];
-        if ((r.rows > 16 && per <= r.rows / 2) || (short_k && r.wn == 1))
+        if ((r.rows > 16 && per <= r.rows / 2) || (short_k && r.wn == 1) || (F32 && r.rows > 64))
             continue;
         const double n = rounds(r.weights, r.rows), cost = n * (r.weights + r.rows * r.wn);
         if ((n <= 1.0 || (!g.offsets && per <= 16.0)) && (best < 0 || cost < least)) {
@@ -877,14 +880,20 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     }
     switch (best) {
     case 0: return launch_ring<KIND, F32, 4, 4, 2, 2>(g, p, st);
-    case 1: return launch_ring<KIND, F32, 4, 4, 4, 2>(g, p, st);
-    case 2: return launch_ring<KIND, F32, 2, 4, 2, 2>(g, p, st);
-    case 3: return launch_ring<KIND, F32, 2, 4, 4, 2>(g, p, st);
-    case 4: return launch_ring<KIND, F32, 2, 2, 4, 2>(g, p, st);
-    case 5: return launch_ring<KIND, F32, 1, 4, 2, 2>(g, p, st);
-    case 6: return launch_ring<KIND, F32, 1, 2, 2, 2>(g, p, st);
-    case 7: return launch_ring<KIND, F32, 1, 2, 4, 2>(g, p, st);
-    case 8:
+    case 1: return launch_ring<KIND, F32, 3, 4, 2, 2>(g, p, st);
+    case 2:
+        if constexpr (!F32)
+            return launch_ring<KIND, F32, 5, 4, 4, 2>(g, p, st);
+        break;
+    case 3: return launch_ring<KIND, F32, 4, 4, 4, 2>(g, p, st);
+    case 4: return launch_ring<KIND, F32, 3, 4, 4, 2>(g, p, st);
+    case 5: return launch_ring<KIND, F32, 2, 4, 2, 2>(g, p, st);
+    case 6: return launch_ring<KIND, F32, 2, 4, 4, 2>(g, p, st);
+    case 7: return launch_ring<KIND, F32, 2, 2, 4, 2>(g, p, st);
+    case 8: return launch_ring<KIND, F32, 1, 4, 2, 2>(g, p, st);
+    case 9: return launch_ring<KIND, F32, 1, 2, 2, 2>(g, p, st);
+    case 10: return launch_ring<KIND, F32, 1, 2, 4, 2>(g, p, st);
+    case 11:
         if constexpr (!SW)
             return launch_ring<KIND, F32, 1, 1, 4, 4>(g, p, st);
     }
