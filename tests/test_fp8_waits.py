@@ -73,9 +73,12 @@ def test_ring_kernel(nsub, tpw, wk, depth, tmp_path):
         if (kind == 0 and tpw == 1) or (f32 and nsub == 5):
             continue
         scales = nsub + (2 if kind == 0 else 1)
-        sym = (f"_ZN3moe12_GLOBAL__N_115fp8_ring_kernelILi{kind}ELb{f32}ELi{nsub}ELi{tpw}ELi{wk}ELi{depth}EEEvNS0_"
-               "7Fp8ArgsEi")
-        ins, copies = checked(cos, sym)
-        assert copies >= depth * copy
-        ahead = (depth - 1) * copy
-        assert ({ahead + scales} if depth == 4 else {ahead, ahead + scales}) <= waits(ins, None), sym
+        for once in (0, 1):
+            if once if nsub > 1 or (kind == 0 and wk > 1) else wk == 1 and not once:
+                continue
+            sym = (f"_ZN3moe12_GLOBAL__N_115fp8_ring_kernelILi{kind}ELb{f32}ELi{nsub}ELi{tpw}ELi{wk}ELi{depth}ELb{once}EEEv"
+                   "NS0_7Fp8ArgsEi")
+            ins, copies = checked(cos, sym)
+            assert copies >= depth * copy
+            ahead = (depth - 1) * copy
+            assert ({ahead + scales} if depth == 4 else {ahead, ahead + scales}) <= waits(ins, None), sym

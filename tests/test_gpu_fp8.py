@@ -94,7 +94,8 @@ MANY_TILES = [(2048, 6160, K) for K in (384, 512, 640, 768, 896, 1024, 1152)]   
 
 
 @pytest.mark.parametrize("M,N,K", MANY_TILES + [(250, 4080, 2176), (333, 2112, 2432), (190, 4080, 2048), (350, 4096, 2176),
-                                                (300, 4000, 512), (450, 2544, 2304), (700, 2048, 2176)])
+                                                (300, 4000, 512), (450, 2544, 2304), (700, 2048, 2176), (9, 7184, 2176),
+                                                (16, 24592, 640), (2, 262144, 256)])
 def test_dense_many_tiles(M, N, K):
     test_dense(M, N, K)
 

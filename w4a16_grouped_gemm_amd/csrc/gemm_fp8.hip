@@ -137,12 +137,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const Fp8Args &p, i
 //
 // Loads to the registers of the lanes that multiply them take 16 bytes of a row
 // each and pass the cache one lane at a time: 16 x 14336 x 4096 17.1 us that way and
-// 14.0 here, 64 x 4096 x 4096 12.1 and 8.7. Where a wave takes all of K (experts with
-// a few rows each, more workgroups than run at a time), the weights come
-// non-temporally, which leaves the caches to the tokens: 128 experts with 4 rows each,
-// 2048 -> 2 x 768, 65 us (6.1 TB/s), in registers 76, there non-temporally 89 (the two
-// halves of a line are fetched apart and the second finds it gone); 4096 -> 2048 168
-// (6.3 TB/s) and 188.
+// 14.2 here, 64 x 4096 x 4096 12.1 and 8.7. Weights that are read once (ONCE) come
+// non-temporally, which leaves the caches to the tokens: 16 x 14336 x 4096 13.2, 1 x
+// 14336 x 4096 11.2 (5.2 TB/s) instead of 12.4; 333 x 2112 x 7168, six chunks to a weight,
+// would take 20.6 instead of 18.0. Experts with a few rows each, more workgroups than
+// run at a time: a wave takes all of K. 128 experts with 4 rows each, 2048 -> 2 x 768, 64 us (6.2
+// TB/s), in registers 76, there non-temporally 89 (the two halves of a line are fetched
+// apart and the second finds it gone); 4096 -> 2048 172 (6.1 TB/s) and 188.
 //
 // Chunks of a dense product side by side on an XCD: 333 x 2112 x 7168 (33 column
 // blocks, which wander over the XCDs else) 22.1 -> 19.7 us; with the multiply-adds
@@ -157,7 +158,7 @@ constexpr int stream_behind(int D, int j, int copies, int scales)
     return (D - 1) * copies + (D == 4 || j == 1 || j == 2 ? scales : 0);
 }
 
-template <int KIND, bool F32, int NSUB, int TPW, int WK, int D>
+template <int KIND, bool F32, int NSUB, int TPW, int WK, int D, bool ONCE>
 __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(Fp8Args p, int blocks)
 {
     constexpr bool SW = KIND == MOE_GEMM_W13_SWIGLU;
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
         const __amdgpu_buffer_rsrc_t rw = make_rsrc(wbase, k < end ? (uint32_t)p.N * p.K : 0u);
 #pragma unroll
         for (int j = 0; j < 2 * TPW; ++j)
-            copy16<WK == 1>(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
+            copy16<ONCE>(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
     };
     auto copy_x = [&](int k, int slot) {
         const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, k < end ? p.a_bytes : 0u);
@@ -385,7 +386,7 @@ void allow_lds()
     });
 }
 
-template <int KIND, bool F32, int NSUB, int TPW, int WK, int D>
+template <int KIND, bool F32, int NSUB, int TPW, int WK, int D, bool ONCE = false>
 hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 {
     constexpr int TG = KIND == MOE_GEMM_W13_SWIGLU ? TPW / 2 : TPW;
@@ -393,10 +394,21 @@ hipError_t launch_ring(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     constexpr int BC = 16 * TG * (4 / WK), kBytes = 4 * D * 2 * (TPW + NSUB) * 1024;
     static_assert(kBytes >= 4 * NSUB * TPW * 1024, "the waves' sums fit");
     const int blocks = (cols + BC - 1) / BC;
-    allow_lds<decltype(fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D>), fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D>, kBytes>();
-    hipLaunchKernelGGL((fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D>),
+    allow_lds<decltype(fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D, ONCE>), fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D, ONCE>,
+              kBytes>();
+    hipLaunchKernelGGL((fp8_ring_kernel<KIND, F32, NSUB, TPW, WK, D, ONCE>),
                        dim3((unsigned)(chunks_at_most(g, 16 * NSUB) * blocks)), dim3(256), kBytes, st, p, blocks);
     return hipGetLastError();
+}
+
+// Tiles of 16 rows; of up to 16 rows in all, the weights are read once.
+template <int KIND, bool F32, int TPW, int WK, int D>
+hipError_t launch_ring_16(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
+{
+    if constexpr (KIND == MOE_GEMM_W2)
+        if (!g.offsets && g.max_rows <= 16)
+            return launch_ring<KIND, F32, 1, TPW, WK, D, true>(g, p, st);
+    return launch_ring<KIND, F32, 1, TPW, WK, D>(g, p, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -890,15 +902,15 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     case 5: return launch_ring<KIND, F32, 2, 4, 2, 2>(g, p, st);
     case 6: return launch_ring<KIND, F32, 2, 4, 4, 2>(g, p, st);
     case 7: return launch_ring<KIND, F32, 2, 2, 4, 2>(g, p, st);
-    case 8: return launch_ring<KIND, F32, 1, 4, 2, 2>(g, p, st);
-    case 9: return launch_ring<KIND, F32, 1, 2, 2, 2>(g, p, st);
-    case 10: return launch_ring<KIND, F32, 1, 2, 4, 2>(g, p, st);
+    case 8: return launch_ring_16<KIND, F32, 4, 2, 2>(g, p, st);
+    case 9: return launch_ring_16<KIND, F32, 2, 2, 2>(g, p, st);
+    case 10: return launch_ring_16<KIND, F32, 2, 4, 2>(g, p, st);
     case 11:
         if constexpr (!SW)
-            return launch_ring<KIND, F32, 1, 1, 4, 4>(g, p, st);
+            return launch_ring_16<KIND, F32, 1, 4, 4>(g, p, st);
     }
     if (g.offsets && per <= 10.0 && (SW || g.K >= 1024))
-        return launch_ring<KIND, F32, 1, 2, 1, 2>(g, p, st);
+        return launch_ring<KIND, F32, 1, 2, 1, 2, true>(g, p, st);
     if (per <= 28.0)
         return launch_tile<KIND, F32, 2, 4>(g, p, st);
     const double rows = g.offsets ? per + 2.0 * sqrt(per) : per, columns = load.items(256, 1) / ceil(per);
