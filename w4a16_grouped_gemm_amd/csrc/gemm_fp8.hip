@@ -12,7 +12,7 @@
 // The matrix unit aligns the products of each run of eight e4m3 pairs to the
 // largest and keeps 13 bits below it (measured, every FP8 instruction alike: a
 // group's sum of normal values is off by 1.5e-5 of itself). bf16 results round at
-// 2^-9, far above; binary32 results take the codes through v_mfma_f32_16x16x32_bf16
+// 2^-8, far above; binary32 results take the codes through v_mfma_f32_16x16x32_bf16
 // instead, whose sums are binary32's.
 #include <mutex>
 

@@ -887,8 +887,10 @@ FP8 = torch.float8_e4m3fn
 
 def _block_scales(shape):
     """A float32 for each 128 values of rows of this shape."""
-    size = (*shape[:-1], shape[-1] // 128)
-    return torch.empty(size, dtype=torch.float32, device="cuda") if len(size) != 2 else _empty(size, (size[1], 1), torch.float32)
+    if len(shape) == 2:
+        rows, K = shape
+        return _empty((rows, K // 128), (K // 128, 1), torch.float32)
+    return torch.empty((*shape[:-1], shape[-1] // 128), dtype=torch.float32, device="cuda")
 
 
 def fp8_quantize(x: torch.Tensor, *, pow2: bool = False, stream=None):
