@@ -392,6 +392,37 @@ def test_captured_and_replayed(T):
         assert same(got, want) and same(got2, want), i
 
 
+def test_replays_with_other_routings():
+    """One captured layer, several tiles to a workgroup: from rows spread evenly over rows of a few experts to none at all."""
+    from w4a16_grouped_gemm_amd import ops
+    T, E, L, k, H, I = 1500, 60, 40, 4, 768, 1024
+    x, ids, w, w13, s13, w2, s2 = layer_inputs(T, E, 0, L, k, H, I, "uniform", 5)
+    xq, xs = ops.fp8_quantize(x)
+
+    def run():
+        return ops.moe_fp8_forward(xq, xs, ids, w, w13, s13, w2, s2, num_experts=E)
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    g = gen(6)
+    local = torch.arange(k, device="cuda", dtype=torch.int32).repeat(T, 1)
+    elsewhere = local + (E - k)
+    one_row = elsewhere.clone()
+    one_row[77] = local[77]
+    for n in (routing(T, E, k, g, "zipf"), local, elsewhere, one_row, routing(T, E, k, g, "uniform")):
+        ids.copy_(n)
+        want = run()
+        torch.cuda.synchronize()
+        got.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        reached = ((n >= 0) & (n < L)).any(1)
+        assert bool((got[~reached] == 0).all()) and bool((got[reached] != 0).any(1).all())
+
+
 def test_two_streams():
     """Two runs at once, each on its own stream: nothing is shared."""
     ins = [block_inputs(T, 16, 256, 384, T) for T in (64, 300)]
