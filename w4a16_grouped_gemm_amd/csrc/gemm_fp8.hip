@@ -441,8 +441,9 @@ hipError_t launch_ring_16(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t 
 //
 // us, tiles of 256 x 128: 4096 x 4096 x 7168 115 (2.1 PFLOP/s), 8192 x 8192 x 8192
 // 482 (2.3), 8192 x 14336 x 4096 452, with a tile to a workgroup 465; 2048 rows on 32
-// experts, 7168 -> 2 x 2048, 180 (940 MB of weights at 5.2 TB/s), 2048 -> 7168 108,
-// with a tile to a workgroup 186 and 111. The large ones are bound by the copies:
+// experts, 7168 -> 2 x 2048, 168 (940 MB of weights at 5.6 TB/s), 2048 -> 7168 100,
+// with weights by way of the caches 180 and 108, and with a tile to a workgroup 186 and
+// 111 then. The large ones are bound by the copies:
 // without them (the operands of the first three groups over and over) the first
 // three take 91, 374 and 364, at the clock that the matrix unit holds; all copies
 // from L2 instead of memory gain 6%.
@@ -860,9 +861,9 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //   R' <= 28: tiles of 128 x 64 (weight rows x tokens): 25 and 32 rows for each of 128 experts, 2048 -> 2 x 768, 72.7 and
 //     75.4; 74.5 and 73.6 with 256 x 64; 80.1 and 78.1 with 256 x 128
 //   above: 256 x 128, but 256 x 64 where that takes no more rounds of the CUs: 1024 x 4096 x 4096 27.4, with 256 x 128 32;
-//     1536 x 4096 x 4096 43.3 and 34.1; 50 rows for each of 128 experts 87.1 and 81.7, where the few experts with more than
-//     64 make a round of their own: the rounds are those of R' and two standard deviations. binary32 results, whose
-//     widened codes need the registers, always 256 x 64: 4096 x 4096 x 4096 141, with 128 x 64 147.
+//     1536 x 4096 x 4096 43.3 and, with 256 x 128, 34.1; 50 rows for each of 128 experts 87.1 and 81.7, where the few
+//     experts with more than 64 make a round of their own: the rounds are those of R' and two standard deviations.
+//     binary32 results, whose widened codes need the registers, always 256 x 64: 4096 x 4096 x 4096 141, with 128 x 64 147.
 template <int KIND, bool F32>
 hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 {
