@@ -163,7 +163,7 @@ def _plain_scale(top, pow2):
     """The scale of blocks whose largest magnitude is `top`: top / 448, or the least power of two that is not less."""
     if pow2:
         m, e = torch.frexp(top)
-        s = torch.exp2((e - 9 + (m > 0.875)).float())            # exact; ldexp is not
+        s = torch.ldexp(torch.ones_like(top), e - 9 + (m > 0.875).int())
     else:
         s = top / TOP
     return torch.where(top >= NOTHING, s, torch.zeros_like(s))
