@@ -152,6 +152,14 @@ __device__ __forceinline__ int count_chunks(const P &p, int CS, int lane, Chunks
     return tm;
 }
 
+// Segments that do not overlap have no more chunks (chunks_at_most on the device). Overlapping ones can have E times as
+// many: a workgroup that takes chunk after chunk of all that are counted stops here.
+template <class P>
+__device__ __forceinline__ int most_chunks(const P &p, int CS)
+{
+    return p.offsets ? p.max_rows / CS + min(p.E, p.max_rows) : (p.max_rows + CS - 1) / CS;
+}
+
 // Where i of n lands so that XCD x, to which workgroups x, x + 8, ... go, takes the x-th share.
 __device__ __forceinline__ int xcd_share(int n, int i)
 {

@@ -504,7 +504,7 @@ __global__ __launch_bounds__(512, TN > 2 ? 2 : 4) void fp8_tile_kernel(Fp8Args p
         const __amdgpu_buffer_rsrc_t ri = index_rsrc(p);
         lds_byte *lds = (lds_byte *)s_dyn;
         Chunks chunks;
-        const int tm = uniform(count_chunks(p, BM, lane, chunks));
+        const int tm = uniform(min(count_chunks(p, BM, lane, chunks), most_chunks(p, BM)));
         // where a tile's copies read from: this lane's rows of weights and tokens, a chunk of each, and of scales
         struct From {
             int e;
