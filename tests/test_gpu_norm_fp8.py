@@ -274,3 +274,17 @@ def test_nothing_to_do():
     assert [tuple(t.shape) for t in ops.add_rms_norm_fp8(x, x, w)] == [(0, 256), (0, 2), (0, 256)]
     assert [tuple(t.shape) for t in ops.fp8_quantize_weights(x)] == [(0, 256), (0, 2)]
     assert [tuple(t.shape) for t in ops.fp8_quantize_weights(x.view(0, 5, 256))] == [(0, 5, 256), (0, 1, 2)]
+
+
+@pytest.mark.parametrize("K", [256, 2048, 7168, 20480])
+def test_norm_of_infinite_eps(K):
+    """Every eps >= 0 is taken. An infinite one makes rows of finite values zeros, codes and scales, as in the int8 norm;
+    a row with a NaN or an infinity still has NaN scales."""
+    from w4a16_grouped_gemm_amd import ops
+    x, _ = rows_of(4, K, K)
+    x[2, 5], x[3, 7] = float("inf"), float("nan")
+    x, w = x.bfloat16().cuda(), torch.ones(K, device="cuda").bfloat16()
+    for pow2 in (False, True):
+        q, s, y = ops.rms_norm_fp8(x, w, eps=float("inf"), pow2=pow2, with_bf16=True)
+        assert bool((q[:2].float() == 0).all()) and bool((s[:2] == 0).all()) and bool((y[:2] == 0).all())
+        assert bool(s[2:].isnan().all())

@@ -69,9 +69,12 @@ __device__ __forceinline__ void scaled_row(const Fp8NormLaunch &n, long long row
         for (int j = 0; j < 8; ++j)
             sq = __builtin_fmaf(h[j] * f, h[j] * f, sq);
     }
-    const float rs = 1.0f / sqrtf(row_sum<TPR>(sq, s_red) / (float)n.K + n.eps * f * f);
+    const float sum = row_sum<TPR>(sq, s_red);
+    const float rs = 1.0f / sqrtf(sum / (float)n.K + n.eps * f * f);
     const float rstd = small ? rs : rs * f, hf = small ? f : 1.0f;
-    const float p2 = small ? power_of(rs) : power_of(rs) * f, m = rs / power_of(rs);
+    const float p2 = small ? power_of(rs) : power_of(rs) * f;
+    // an infinite eps makes rs 0, and finite rows zeros; a row with an infinity is NaN
+    const float m = rs == 0.0f && __builtin_isfinite(sum) ? 1.0f : rs / power_of(rs);
 #pragma unroll 1
     for (uint32_t o = lane * 16; o < bytes; o += TPR * 16) {
         float h[8], g[8], u[8];
