@@ -78,10 +78,11 @@ __device__ __forceinline__ int scan_chunks(const P &p, uint32_t CS, int lane, in
     return before;
 }
 
-// Chunk `chunk`, where it is one of c's: its expert, first row and rows.
+// Chunk `chunk`, where it is one of c's: its expert, first row and rows; in only, where asked for, whether the expert has
+// no other.
 template <class P>
 __device__ __forceinline__ bool pick_chunk(const P &p, int CS, int e0, int chunk, const Chunks &c, int &e, int &r0,
-                                           int &rows)
+                                           int &rows, bool *only = nullptr)
 {
     bool found = false;
 #pragma unroll
@@ -95,6 +96,8 @@ __device__ __forceinline__ bool pick_chunk(const P &p, int CS, int e0, int chunk
             const int end = min(__builtin_amdgcn_readlane(c.o1[i], l), p.max_rows);
             found = r0 >= 0 && r0 < end;               // compared: a difference could pass 32 bits
             rows = end - r0;
+            if (only)
+                *only = __builtin_amdgcn_readlane(c.n[i], l) == 1;
         }
     }
     rows = rows < CS ? rows : CS;
@@ -114,8 +117,11 @@ __device__ __forceinline__ bool dense_chunk(const P &p, int CS, int chunk, int &
 // Chunk `chunk`: its expert, first row and rows; false past the last chunk. One
 // wave, every lane gets the result.
 template <bool CLAMP, class P>
-__device__ __forceinline__ bool find_chunk(const P &p, int CS, int chunk, int lane, int &e, int &r0, int &rows)
+__device__ __forceinline__ bool find_chunk(const P &p, int CS, int chunk, int lane, int &e, int &r0, int &rows,
+                                           bool *only = nullptr)
 {
+    if (only)
+        *only = p.max_rows <= CS;
     if (!p.offsets)
         return dense_chunk(p, CS, chunk, e, r0, rows);
     e = r0 = rows = 0;
@@ -123,7 +129,7 @@ __device__ __forceinline__ bool find_chunk(const P &p, int CS, int chunk, int la
         Chunks c;
         before = scan_chunks<CLAMP>(p, CS, lane, e0, before, c);
         if (chunk < before)
-            return pick_chunk(p, CS, e0, chunk, c, e, r0, rows);
+            return pick_chunk(p, CS, e0, chunk, c, e, r0, rows, only);
     }
     return false;
 }

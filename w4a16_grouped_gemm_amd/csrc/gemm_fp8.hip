@@ -153,7 +153,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const Fp8Args &p, i
 // would take 20.6 instead of 18.0. Experts with a few rows each, more workgroups than
 // run at a time: a wave takes all of K. 128 experts with 4 rows each, 2048 -> 2 x 768, 64 us (6.2
 // TB/s), in registers 76, there non-temporally 89 (the two halves of a line are fetched
-// apart and the second finds it gone); 4096 -> 2048 172 (6.1 TB/s) and 188.
+// apart and the second finds it gone); 4096 -> 2048 172 (6.1 TB/s) and 188. Of these an
+// expert with several chunks has its weights read by each of them, so by way of the
+// caches: 64 and 100 tokens on 128 experts by Zipf's law (up to 64 and 99 rows for one)
+// 57.3 us instead of 58.9, 65.8 instead of 68.9, 32 tokens on 32 experts of 7168 -> 2 x 2048
+// 158 instead of 175, 2048 -> 7168 75 instead of 83, but 768 -> 2048 34.4 instead of 34.1
+// and 41.8 instead of 40.2. Two loops, since a choice at each copy took 1 us of 50.
 //
 // Chunks of a dense product side by side on an XCD: 333 x 2112 x 7168 (33 column
 // blocks, which wander over the XCDs else) 22.1 -> 19.7 us; with the multiply-adds
@@ -190,7 +195,8 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
         chunk = i - block * chunks;
     }
     int e, r0, rows;
-    if (!find_chunk<false>(p, 16 * NSUB, chunk, lane, e, r0, rows))
+    bool once = ONCE;                                   // the weights come non-temporally: where the expert has one chunk
+    if (!find_chunk<false>(p, 16 * NSUB, chunk, lane, e, r0, rows, ONCE && WK == 1 ? &once : nullptr))
         return;
     e = uniform(e);
     const int cols = SW ? p.N / 2 : p.N;                // outputs per row
@@ -229,11 +235,11 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
     int g = wk * G / WK;
     const int end = (wk + 1) * G / WK;
     lds_byte *lds = (lds_byte *)s_dyn + wave * kWave;
-    auto copy_w = [&](int k, int slot) {
+    auto copy_w = [&](auto nt, int k, int slot) {
         const __amdgpu_buffer_rsrc_t rw = make_rsrc(wbase, k < end ? (uint32_t)p.N * p.K : 0u);
 #pragma unroll
         for (int j = 0; j < 2 * TPW; ++j)
-            copy16<ONCE>(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
+            copy16<decltype(nt)::value>(rw, lds + slot * kSlot + j * 1024, wo[j], k < end ? k * 128 : 0);
     };
     auto copy_x = [&](int k, int slot) {
         const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.a, k < end ? p.a_bytes : 0u);
@@ -253,7 +259,8 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
             s.w[1] = __builtin_bit_cast(floatx4, bload16(rws, ws1 + k * 4, 0));
     };
     // the first weights set out before the tokens' rows are known
-    copy_w(g, 0);
+    const std::integral_constant<bool, ONCE> first{};   // these non-temporally in any case
+    copy_w(first, g, 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 2 * NSUB; ++j)
@@ -273,7 +280,7 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 1; j < D; ++j) {
-        copy_w(g + j, j);
+        copy_w(first, g + j, j);
         copy_x(g + j, j);
     }
     floatx4 acc[NSUB][TPW];
@@ -290,7 +297,7 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
         f.hi = *reinterpret_cast<const u32x4 *>(s_dyn + (f0 ^ 64u) + slot * kSlot + i * 2048);
         return f;
     };
-    auto turn = [&](auto turn_of) {
+    auto turn = [&](auto nt, auto turn_of) {
         constexpr int J = decltype(turn_of)::value, SLOT = J % D;
         wait_for<stream_behind(D, J, C, kScales)>();
         if (g + J < end) {
@@ -323,20 +330,26 @@ __global__ __launch_bounds__(256, NSUB * TPW > 8 ? 1 : 2) void fp8_ring_kernel(F
         }
         // every fragment has left LDS
         __builtin_amdgcn_sched_barrier(0);
-        copy_w(g + J + D, SLOT);
+        copy_w(nt, g + J + D, SLOT);
         copy_x(g + J + D, SLOT);
         __builtin_amdgcn_sched_barrier(0);
     };
-    for (; g < end; g += 4) {
-        turn(std::integral_constant<int, 0>());
-        load_scales(sl, g + 8);
-        __builtin_amdgcn_sched_barrier(0);
-        turn(std::integral_constant<int, 1>());
-        turn(std::integral_constant<int, 2>());
-        turn(std::integral_constant<int, 3>());
-        sc = sn;
-        sn = sl;
-    }
+    auto groups = [&](auto nt) {
+        for (; g < end; g += 4) {
+            turn(nt, std::integral_constant<int, 0>());
+            load_scales(sl, g + 8);
+            __builtin_amdgcn_sched_barrier(0);
+            turn(nt, std::integral_constant<int, 1>());
+            turn(nt, std::integral_constant<int, 2>());
+            turn(nt, std::integral_constant<int, 3>());
+            sc = sn;
+            sn = sl;
+        }
+    };
+    if (once)
+        groups(std::true_type());
+    else
+        groups(std::false_type());
     wait_for<0>();                                      // copies past the last group write to LDS too
     if constexpr (WK > 1) {
         floatx4 *part = reinterpret_cast<floatx4 *>(s_dyn);   // [WN][WK - 1][NSUB TPW][64]
