@@ -556,6 +556,10 @@ moe_status moe_grouped_gemm_fp8(const moe_shape *shape, moe_gemm_kind kind, cons
  *   x uint8 [T][H], x_scale f32 [T][H/128], out bf16 [T][H] (+0.0 for a token with
  *   no local slot); workspace >= moe_fp8_workspace_size bytes (0 for an invalid
  *   shape), 256-B aligned, no state between calls.
+ * A gate/up value that its sum's error takes over the middle of two codes becomes
+ * another code. Against the definition in 64 bits the layer's mean square error is
+ * that of the result's rounding where the products add in binary32 (few rows, as
+ * above: 1.65e-3 of the result), and 2.0e-3 to 2.4e-3 with the FP8 instruction's sums.
  */
 size_t moe_fp8_workspace_size(const moe_shape *shape);
 moe_status moe_fp8_forward(const moe_shape *shape, const uint8_t *x, const float *x_scale, const int32_t *topk_ids,
