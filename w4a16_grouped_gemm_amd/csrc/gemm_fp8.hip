@@ -876,13 +876,18 @@ hipError_t launch_tile(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
 //     4096 14.7 with 64 x 64, 18.1 with 32 x 64; 350 x 4096 x 4096 17.6 with 48 x 128, 20.2 with 64 x 128; 450 x 2560 x 4096
 //     15.7 with 80 x 64, 17.1 with 48 x 128; 512 x 4096 x 4096 21.0 with 64 x 128, 26.1 with 64 x 64 and 24.5 in the
 //     tile kernel; 333 x 2112 x 7168 18.0 with 48 x 64, 19.3 with 64 x 64 and 41 in the tile kernel. 80 rows of binary32
-//     results spill. Half of K to a wave instead of a quarter where K is short: 333 x 2112 x 768 6.5 against 8.1.
+//     results spill. From 17 rows on, half of K to a wave instead of a quarter where K is short: 64 x 4096 x 512, 1024, 1280
+//     and 1920 4.0, 4.4, 5.2 and 6.1 against 4.7, 4.8, 5.0 and 5.7, 256 x 4096 x the same 6.2, 6.6, 8.6 and 9.9 against 7.7,
+//     8.0, 8.4 and 9.4, 333 x 2112 x 512, 1024 and 1280 6.0, 6.5 and 8.4 against 6.5, 6.8 and 7.2. (Up to 16 rows
+//     a quarter is better at any K: 1 x 4096 x 512, 1024 and 1920 3.7, 3.8 and 4.1 against 3.9, 4.5 and 6.3.)
 //     With up to 16 rows of a dense product at any number of columns.
 //   experts with R' <= 10: the ring kernel with 16 x 32 weight rows to a wave, all of K, whose sums are binary32's too (TB/s of
 //     all that is read and written, here and in tiles of 128 x 64): 2048 -> 2 x 768 with 1, 4, 8 and 16 rows for each of 128
 //     experts 5.8 and 5.4, 6.0 and 5.8, 6.1 and 5.8, 4.5 and 5.6; 2048 -> 2048 with 4 rows 6.3 and 6.0, 1024 -> 2048 5.9 and
-//     5.7. Shorter K, us: 768 -> 2048 with 1, 4 and 8 rows 28.2 and 27.4, 38.8 and 36.4, 41.2 and 37.1; 512 -> 2048 with 4
-//     and 8 26.9 and 26.9, 28.4 and 26.9; 256 -> 2048 with 4 22.1 and 24.0, 256 -> 7168 of 256 experts with 1 46.7 and 54.3
+//     5.7. Shorter K, us: 128, 256, 512 and 1024 -> 2 x 768 with 8 rows 16.1 and 15.0, 17.5 and 19.4, 22.2 and 22.3, 36.4 and
+//     38.1, with 10 rows 17.3 and 15.2, 19.0 and 19.6, 23.1 and 21.6, 38.6 and 37.7; 768 -> 2048 with 1, 4 and 8 rows 28.2
+//     and 27.4, 38.8 and 36.4, 41.2 and 37.1; 512 -> 2048 with 4 and 8 26.9 and 26.9, 28.4 and 26.9; 256 -> 2048 with 4 22.1
+//     and 24.0, 256 -> 7168 of 256 experts with 1 46.7 and 54.3
 //   R' <= 28: tiles of 128 x 64 (weight rows x tokens): 25 and 32 rows for each of 128 experts, 2048 -> 2 x 768, 72.7 and
 //     75.4; 74.5 and 73.6 with 256 x 64; 80.1 and 78.1 with 256 x 128
 //   above: 256 x 128, but 256 x 64 where that takes no more rounds of the CUs: 1024 x 4096 x 4096 27.4, with 256 x 128 32;
@@ -903,12 +908,12 @@ hipError_t launch_kind(const Fp8GemmLaunch &g, const Fp8Args &p, hipStream_t st)
     };
     constexpr Ring kRing[] = {{64, 128, 2}, {48, 128, 2}, {80, 64, 1}, {64, 64, 1}, {48, 64, 1}, {32, 128, 2},
                               {32, 64, 1}, {32, 32, 1}, {16, 128, 2}, {16, 64, 2}, {16, 32, 1}, {16, 16, 1}};
-    const bool short_k = g.K < 2048;
+    const bool short_k = g.K <= 1024;
     int best = -1;
     double least = 0.0;
     for (int i = 0; i < (SW ? 11 : 12); ++i) {
         const Ring &r = kRing[i];
-        if ((r.rows > 16 && per <= r.rows / 2) || (short_k && r.wn == 1) || (F32 && r.rows > 64))
+        if ((r.rows > 16 && (per <= r.rows / 2 || (short_k && r.wn == 1))) || (F32 && r.rows > 64))
             continue;
         const double n = rounds(r.weights, r.rows), cost = n * (r.weights + r.rows * r.wn);
         if ((n <= 1.0 || (!g.offsets && per <= 16.0)) && (best < 0 || cost < least)) {
